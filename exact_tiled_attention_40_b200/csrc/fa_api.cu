@@ -119,6 +119,19 @@ int encode_tensor_map_u8(CUtensorMap* m, const void* base, int rank, const uint6
                            box);
 }
 
+int raise_smem_limit(const void* kernel, int bytes, int device, SmemKernel which) {
+  static int gen[kSmemKernels][64] = {};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> g(mu);
+  if (device < 0 || device >= 64) return set_error(FA_ERR_CUDA, "device ordinal out of range");
+  if (gen[which][device] == cache_generation()) return FA_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess)
+    return set_error(FA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  gen[which][device] = cache_generation();
+  return FA_OK;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -348,10 +361,409 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
                     causal, stream, dev);
 }
 
+bool aligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// A span of device memory, for refusing outputs that overlap inputs.
+struct Span {
+  uintptr_t at;
+  unsigned long long bytes;
+};
+Span rows_span(const void* p, long long rows, long long stride, long long width) {
+  return {reinterpret_cast<uintptr_t>(p),
+          p && rows > 0 && width > 0
+              ? static_cast<unsigned long long>((rows - 1) * stride + width) * 2
+              : 0};
+}
+bool overlap(const Span& a, const Span& b) {
+  return a.bytes && b.bytes && a.at < b.at + b.bytes && b.at < a.at + a.bytes;
+}
+
+// Rules shared by the norm + rotation entry points.
+int validate_norm_rope(const NormRopeArgs& a, long long tokens) {
+  if (a.Hq < 0 || a.Hkv < 0) return set_error(FA_ERR_INVALID_ARG, "negative size");
+  if (a.D != 64 && a.D != 128)
+    return set_error(FA_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", a.D);
+  if (a.rot_dim < 0 || a.rot_dim > a.D || a.rot_dim % 16 != 0)
+    return set_error(FA_ERR_UNSUPPORTED, "rot_dim %d not supported (a multiple of 16 up to D = %d)",
+                     a.rot_dim, a.D);
+  if ((a.q_weight || a.k_weight) && !(std::isfinite(a.eps) && a.eps > 0.f))
+    return set_error(FA_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (a.n_axes < 1 || a.n_axes > 8)
+    return set_error(FA_ERR_UNSUPPORTED, "n_axes %d not supported (1 to 8)", a.n_axes);
+  if (a.rot_dim > 0 && a.max_pos <= 0)
+    return set_error(FA_ERR_INVALID_ARG, "max_positions must be positive");
+  if (tokens > 0x7fffffffLL ||
+      tokens * (static_cast<long long>(a.Hq) + 2LL * a.Hkv) > 0x7fffffffLL)
+    return set_error(FA_ERR_UNSUPPORTED, "too many head rows for one call");
+  if (!aligned16(a.q_weight) || !aligned16(a.k_weight) || !aligned16(a.table))
+    return set_error(FA_ERR_INVALID_ARG, "weights and table must be 16-byte aligned");
+  if (!aligned(a.positions, 4)) return set_error(FA_ERR_INVALID_ARG, "positions misaligned");
+  if (tokens == 0) return FA_OK;
+  if (a.rot_dim > 0 && (!a.table || !a.positions || (a.n_axes > 1 && !a.pair_axis)))
+    return set_error(FA_ERR_INVALID_ARG, "null table, positions or pair_axis");
+  return FA_OK;
+}
+
+// Token-major rows [tokens, H, D] with `stride` elements between tokens.
+int validate_rows(const char* what, const void* p, long long stride, int H, int D) {
+  if (H == 0) return FA_OK;
+  if (!p) return set_error(FA_ERR_INVALID_ARG, "null pointer (%s)", what);
+  if (!aligned16(p)) return set_error(FA_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  if (stride < static_cast<long long>(H) * D || stride % 8 != 0 || stride > (1LL << 31))
+    return set_error(FA_ERR_INVALID_ARG,
+                     "%s: the token stride (%lld) must be a multiple of 8 elements, at least H * D",
+                     what, stride);
+  return FA_OK;
+}
+
+int norm_rope_common(NormRopeArgs a, int B, cudaStream_t stream) {
+  if (B < 0 || a.N < 0) return set_error(FA_ERR_INVALID_ARG, "negative size");
+  const long long tokens = static_cast<long long>(B) * a.N;
+  int rc = validate_norm_rope(a, tokens);
+  if (rc != FA_OK) return rc;
+  if (tokens == 0 || (a.Hq == 0 && a.Hkv == 0)) return FA_OK;
+  const long long qw = static_cast<long long>(a.Hq) * a.D, kw = static_cast<long long>(a.Hkv) * a.D;
+  if ((rc = validate_rows("q", a.q, a.q_stride, a.Hq, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("k", a.k, a.k_stride, a.Hkv, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("q_out", a.q_out, qw, a.Hq, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("k_out", a.k_out, kw, a.Hkv, a.D)) != FA_OK) return rc;
+  const Span in[2] = {rows_span(a.q, tokens, a.q_stride, qw), rows_span(a.k, tokens, a.k_stride, kw)};
+  const Span out[2] = {rows_span(a.q_out, tokens, qw, qw), rows_span(a.k_out, tokens, kw, kw)};
+  if (overlap(in[0], out[0]) || overlap(in[0], out[1]) || overlap(in[1], out[0]) ||
+      overlap(in[1], out[1]) || overlap(out[0], out[1]))
+    return set_error(FA_ERR_INVALID_ARG, "outputs must not overlap the inputs or each other");
+  int dev;
+  if ((rc = current_sm100(&dev)) != FA_OK) return rc;
+  a.T = static_cast<int>(tokens);
+  return launch_norm_rope(a, stream, dev);
+}
+
+int norm_rope_bwd_common(NormRopeArgs a, const NormRopeGrads& g, int B, cudaStream_t stream) {
+  if (B < 0 || a.N < 0) return set_error(FA_ERR_INVALID_ARG, "negative size");
+  const long long tokens = static_cast<long long>(B) * a.N;
+  int rc = validate_norm_rope(a, tokens);
+  if (rc != FA_OK) return rc;
+  if ((a.q_weight && !g.dq_weight) || (a.k_weight && !g.dk_weight) ||
+      ((a.q_weight || a.k_weight) && !g.scratch))
+    return set_error(FA_ERR_INVALID_ARG, "null weight gradient or scratch");
+  if (!aligned16(g.dq_weight) || !aligned16(g.dk_weight) || !aligned16(g.scratch))
+    return set_error(FA_ERR_INVALID_ARG, "weight gradients and scratch must be 16-byte aligned");
+  const bool rows = tokens > 0 && (a.Hq > 0 || a.Hkv > 0);
+  if (!rows && !a.q_weight && !a.k_weight) return FA_OK;
+  if (rows) {
+    const long long qw = static_cast<long long>(a.Hq) * a.D,
+                    kw = static_cast<long long>(a.Hkv) * a.D;
+    if ((rc = validate_rows("q", a.q, a.q_stride, a.Hq, a.D)) != FA_OK) return rc;
+    if ((rc = validate_rows("k", a.k, a.k_stride, a.Hkv, a.D)) != FA_OK) return rc;
+    if ((rc = validate_rows("dq_out", g.dq_out, qw, a.Hq, a.D)) != FA_OK) return rc;
+    if ((rc = validate_rows("dk_out", g.dk_out, kw, a.Hkv, a.D)) != FA_OK) return rc;
+    if ((rc = validate_rows("dq", g.dq, g.dq_stride, a.Hq, a.D)) != FA_OK) return rc;
+    if ((rc = validate_rows("dk", g.dk, g.dk_stride, a.Hkv, a.D)) != FA_OK) return rc;
+    const Span in[4] = {rows_span(a.q, tokens, a.q_stride, qw),
+                        rows_span(a.k, tokens, a.k_stride, kw),
+                        rows_span(g.dq_out, tokens, qw, qw), rows_span(g.dk_out, tokens, kw, kw)};
+    // (dq and dk may interleave: views of one gradient of the whole projection)
+    const Span out[2] = {rows_span(g.dq, tokens, g.dq_stride, qw),
+                         rows_span(g.dk, tokens, g.dk_stride, kw)};
+    for (const Span& i : in)
+      for (const Span& o : out)
+        if (overlap(i, o))
+          return set_error(FA_ERR_INVALID_ARG, "outputs must not overlap the inputs");
+  } else {
+    a.Hq = a.Hkv = 0;            // only the weight gradients, which are zero
+  }
+  int dev;
+  if ((rc = current_sm100(&dev)) != FA_OK) return rc;
+  a.T = rows ? static_cast<int>(tokens) : 0;
+  return launch_norm_rope_bwd(a, g, stream, dev);
+}
+
+int append_common(NormRopeArgs a, int page_size, int num_pages, cudaStream_t stream) {
+  if (a.T < 0 || num_pages < 0) return set_error(FA_ERR_INVALID_ARG, "negative size");
+  if (page_size != 16)
+    return set_error(FA_ERR_UNSUPPORTED, "the page pool has page_size == 16 only (got %d)",
+                     page_size);
+  int rc = validate_norm_rope(a, a.T);
+  if (rc != FA_OK) return rc;
+  if (a.T == 0 || (a.Hq == 0 && a.Hkv == 0)) return FA_OK;
+  if (!a.slot_map || !aligned(a.slot_map, 8))
+    return set_error(FA_ERR_INVALID_ARG, "slot_map null or misaligned");
+  if (num_pages <= 0) return set_error(FA_ERR_INVALID_ARG, "num_pages must be positive");
+  const long long qw = static_cast<long long>(a.Hq) * a.D, kw = static_cast<long long>(a.Hkv) * a.D;
+  a.num_slots = static_cast<long long>(num_pages) * page_size;
+  if ((rc = validate_rows("q", a.q, a.q_stride, a.Hq, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("k", a.k, a.k_stride, a.Hkv, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("v", a.v, a.v_stride, a.Hkv, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("q_out", a.q_out, qw, a.Hq, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("kcache", a.k_out, kw, a.Hkv, a.D)) != FA_OK) return rc;
+  if ((rc = validate_rows("vcache", a.v_out, kw, a.Hkv, a.D)) != FA_OK) return rc;
+  const Span in[3] = {rows_span(a.q, a.T, a.q_stride, qw), rows_span(a.k, a.T, a.k_stride, kw),
+                      rows_span(a.v, a.T, a.v_stride, kw)};
+  const Span out[3] = {rows_span(a.q_out, a.T, qw, qw), rows_span(a.k_out, a.num_slots, kw, kw),
+                       rows_span(a.v_out, a.num_slots, kw, kw)};
+  for (const Span& i : in)
+    for (const Span& o : out)
+      if (overlap(i, o))
+        return set_error(FA_ERR_INVALID_ARG, "q_out and the caches must not overlap the inputs");
+  if (overlap(out[0], out[1]) || overlap(out[0], out[2]) || overlap(out[1], out[2]))
+    return set_error(FA_ERR_INVALID_ARG, "q_out, kcache and vcache must not overlap");
+  int dev;
+  if ((rc = current_sm100(&dev)) != FA_OK) return rc;
+  return launch_norm_rope(a, stream, dev);
+}
+
+int extend_common(const ExtendArgs& a, int page_size, cudaStream_t stream) {
+  if (a.B < 0 || a.max_pages_per_seq < 0 || a.num_pages < 0 || a.max_tokens < 0)
+    return set_error(FA_ERR_INVALID_ARG, "negative size");
+  if (page_size != 16)
+    return set_error(FA_ERR_UNSUPPORTED, "the page pool has page_size == 16 only (got %d)",
+                     page_size);
+  if (a.B > kMaxExtendSeqs)
+    return set_error(FA_ERR_UNSUPPORTED, "B (%d) above %d", a.B, kMaxExtendSeqs);
+  if (a.max_pages_per_seq > 0x7fffffff / 16 || a.num_pages > 0x7fffffff / 16)
+    return set_error(FA_ERR_INVALID_ARG, "sizes too large");
+  if (a.B > 0 && (a.max_pages_per_seq == 0 || a.num_pages == 0))
+    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq and num_pages must be positive");
+  if (!a.free_count || !a.free_count_out || !a.cu_seqlens_q ||
+      (a.B > 0 && (!a.block_table || !a.seq_lens || !a.new_lens || !a.free_pages ||
+                   !a.seq_lens_out)) ||
+      (a.max_tokens > 0 && (!a.positions || !a.slot_map)))
+    return set_error(FA_ERR_INVALID_ARG, "null pointer");
+  for (const void* p : {static_cast<const void*>(a.block_table), static_cast<const void*>(a.seq_lens),
+                        static_cast<const void*>(a.new_lens), static_cast<const void*>(a.free_pages),
+                        static_cast<const void*>(a.free_count),
+                        static_cast<const void*>(a.seq_lens_out),
+                        static_cast<const void*>(a.free_count_out),
+                        static_cast<const void*>(a.cu_seqlens_q),
+                        static_cast<const void*>(a.positions)})
+    if (!aligned(p, 4)) return set_error(FA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (!aligned(a.slot_map, 8))
+    return set_error(FA_ERR_INVALID_ARG, "slot_map must be 8-byte aligned");
+  int dev, rc;
+  if ((rc = current_sm100(&dev)) != FA_OK) return rc;
+  return launch_extend_pages(a, stream, dev);
+}
+
+// Rules of the paged decode entry points; FA_OK also for empty problems.
+int validate_decode(const void* q, const void* kcache, const void* vcache,
+                    const int32_t* block_table, const int32_t* seq_lens, const void* o, int B,
+                    int Hq, int Hkv, int D, int page_size, float scale, int max_pages_per_seq,
+                    int num_pages) {
+  if (B < 0 || Hq < 0 || Hkv < 0 || max_pages_per_seq < 0 || num_pages < 0)
+    return set_error(FA_ERR_INVALID_ARG, "negative size");
+  if (!(std::isfinite(scale) && scale > 0.f))
+    return set_error(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (D != 128) return set_error(FA_ERR_UNSUPPORTED, "decode supports D == 128 only (got %d)", D);
+  if (page_size != 16)
+    return set_error(FA_ERR_UNSUPPORTED, "decode supports page_size == 16 only (got %d)",
+                     page_size);
+  if (B == 0 || Hq == 0) return FA_OK;
+  if (Hkv <= 0 || Hq % Hkv != 0)
+    return set_error(FA_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d)", Hq,
+                     Hkv);
+  const int G = Hq / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8)
+    return set_error(FA_ERR_UNSUPPORTED, "decode supports Hq/Hkv in {1,2,4,8} (got %d)", G);
+  if (max_pages_per_seq <= 0 || num_pages <= 0)
+    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq and num_pages must be positive");
+  if (!q || !kcache || !vcache || !block_table || !seq_lens || !o)
+    return set_error(FA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(o))
+    return set_error(FA_ERR_INVALID_ARG, "q, caches and o must be 16-byte aligned");
+  if (static_cast<long long>(max_pages_per_seq) * 16 > 0x7fffffffLL)
+    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq too large");
+  return FA_OK;
+}
+
 }  // namespace
 }  // namespace fa
 
 extern "C" {
+
+static int norm_rope_entry(const void* q, const void* k, const void* q_weight,
+                           const void* k_weight, const float* table, const int32_t* positions,
+                           const uint8_t* pair_axis, void* q_out, void* k_out, int B, int N,
+                           int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                           int rot_dim, int max_positions, int n_axes, int interleaved,
+                           int heads_first, float eps, fa_stream_t stream, bool bf16) {
+  fa::NormRopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.table = table;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.rot_dim = rot_dim;
+  a.max_pos = max_positions;
+  a.n_axes = n_axes;
+  a.interleaved = interleaved != 0;
+  a.heads_first = heads_first != 0;
+  a.bf16 = bf16;
+  a.eps = eps;
+  return fa::norm_rope_common(a, B, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int norm_rope_bwd_entry(const void* q, const void* k, const void* dq_out,
+                               const void* dk_out, const void* q_weight, const void* k_weight,
+                               const float* table, const int32_t* positions,
+                               const uint8_t* pair_axis, void* dq, void* dk, float* dq_weight,
+                               float* dk_weight, float* scratch, int B, int N, int Hq, int Hkv,
+                               int D, long long q_stride, long long k_stride,
+                               long long dq_stride, long long dk_stride, int rot_dim,
+                               int max_positions, int n_axes, int interleaved, int heads_first,
+                               float eps, fa_stream_t stream, bool bf16) {
+  fa::NormRopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.table = table;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.rot_dim = rot_dim;
+  a.max_pos = max_positions;
+  a.n_axes = n_axes;
+  a.interleaved = interleaved != 0;
+  a.heads_first = heads_first != 0;
+  a.bf16 = bf16;
+  a.eps = eps;
+  fa::NormRopeGrads g;
+  g.dq_out = dq_out;
+  g.dk_out = dk_out;
+  g.dq = dq;
+  g.dk = dk;
+  g.dq_stride = dq_stride;
+  g.dk_stride = dk_stride;
+  g.dq_weight = dq_weight;
+  g.dk_weight = dk_weight;
+  g.scratch = scratch;
+  return fa::norm_rope_bwd_common(a, g, B, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                    const float* table, const int32_t* positions, const uint8_t* pair_axis,
+                    void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int D,
+                    long long q_stride, long long k_stride, int rot_dim, int max_positions,
+                    int n_axes, int interleaved, int heads_first, float eps, fa_stream_t stream) {
+  return norm_rope_entry(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N,
+                         Hq, Hkv, D, q_stride, k_stride, rot_dim, max_positions, n_axes,
+                         interleaved, heads_first, eps, stream, true);
+}
+
+int fa_qk_norm_rope_fp16(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                         const float* table, const int32_t* positions, const uint8_t* pair_axis,
+                         void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int D,
+                         long long q_stride, long long k_stride, int rot_dim, int max_positions,
+                         int n_axes, int interleaved, int heads_first, float eps,
+                         fa_stream_t stream) {
+  return norm_rope_entry(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N,
+                         Hq, Hkv, D, q_stride, k_stride, rot_dim, max_positions, n_axes,
+                         interleaved, heads_first, eps, stream, false);
+}
+
+int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                        const void* q_weight, const void* k_weight, const float* table,
+                        const int32_t* positions, const uint8_t* pair_axis, void* dq, void* dk,
+                        float* dq_weight, float* dk_weight, float* scratch, int B, int N, int Hq,
+                        int Hkv, int D, long long q_stride, long long k_stride,
+                        long long dq_stride, long long dk_stride, int rot_dim, int max_positions,
+                        int n_axes, int interleaved, int heads_first, float eps,
+                        fa_stream_t stream) {
+  return norm_rope_bwd_entry(q, k, dq_out, dk_out, q_weight, k_weight, table, positions, pair_axis,
+                             dq, dk, dq_weight, dk_weight, scratch, B, N, Hq, Hkv, D, q_stride,
+                             k_stride, dq_stride, dk_stride, rot_dim, max_positions, n_axes,
+                             interleaved, heads_first, eps, stream, true);
+}
+
+int fa_qk_norm_rope_bwd_fp16(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                             const void* q_weight, const void* k_weight, const float* table,
+                             const int32_t* positions, const uint8_t* pair_axis, void* dq,
+                             void* dk, float* dq_weight, float* dk_weight, float* scratch, int B,
+                             int N, int Hq, int Hkv, int D, long long q_stride,
+                             long long k_stride, long long dq_stride, long long dk_stride,
+                             int rot_dim, int max_positions, int n_axes, int interleaved,
+                             int heads_first, float eps, fa_stream_t stream) {
+  return norm_rope_bwd_entry(q, k, dq_out, dk_out, q_weight, k_weight, table, positions, pair_axis,
+                             dq, dk, dq_weight, dk_weight, scratch, B, N, Hq, Hkv, D, q_stride,
+                             k_stride, dq_stride, dk_stride, rot_dim, max_positions, n_axes,
+                             interleaved, heads_first, eps, stream, false);
+}
+
+int fa_append_paged(const void* q, const void* k, const void* v, const void* q_weight,
+                    const void* k_weight, const float* table, const int32_t* positions,
+                    const uint8_t* pair_axis, const int64_t* slot_map, void* q_out, void* kcache,
+                    void* vcache, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
+                    long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                    int max_positions, int n_axes, int interleaved, float eps,
+                    fa_stream_t stream) {
+  fa::NormRopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.table = table;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.slot_map = slot_map;
+  a.q_out = q_out;
+  a.k_out = kcache;
+  a.v_out = vcache;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rot_dim = rot_dim;
+  a.max_pos = max_positions;
+  a.n_axes = n_axes;
+  a.interleaved = interleaved != 0;
+  a.bf16 = true;
+  a.eps = eps;
+  return fa::append_common(a, page_size, num_pages, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_extend_pages(int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
+                    const int32_t* free_pages, const int32_t* free_count, int32_t* seq_lens_out,
+                    int32_t* free_count_out, int32_t* cu_seqlens_q, int32_t* positions,
+                    int64_t* slot_map, int B, int max_pages_per_seq, int num_pages, int page_size,
+                    int max_tokens, fa_stream_t stream) {
+  fa::ExtendArgs a;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.seq_lens_out = seq_lens_out;
+  a.free_count_out = free_count_out;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.positions = positions;
+  a.slot_map = slot_map;
+  a.B = B;
+  a.max_pages_per_seq = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.max_tokens = max_tokens;
+  return fa::extend_common(a, page_size, reinterpret_cast<cudaStream_t>(stream));
+}
 
 int fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
            const void* dout, void* dq, void* dk, void* dv, float* delta, int B, int Hq, int Hkv,
@@ -433,30 +845,11 @@ int fa_decode_paged(const void* q, const void* kcache, const void* vcache,
                     int Hkv, int D, int page_size, float scale, fa_stream_t stream,
                     int max_pages_per_seq, int num_pages, float* lse) {
   using namespace fa;
-  if (B < 0 || Hq < 0 || Hkv < 0 || max_pages_per_seq < 0 || num_pages < 0)
-    return set_error(FA_ERR_INVALID_ARG, "negative size");
-  if (!(std::isfinite(scale) && scale > 0.f))
-    return set_error(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
-  if (D != 128) return set_error(FA_ERR_UNSUPPORTED, "decode supports D == 128 only (got %d)", D);
-  if (page_size != 16)
-    return set_error(FA_ERR_UNSUPPORTED, "decode supports page_size == 16 only (got %d)",
-                     page_size);
-  if (B == 0 || Hq == 0) return FA_OK;
-  if (Hkv <= 0 || Hq % Hkv != 0)
-    return set_error(FA_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d)", Hq,
-                     Hkv);
-  const int G = Hq / Hkv;
-  if (G != 1 && G != 2 && G != 4 && G != 8)
-    return set_error(FA_ERR_UNSUPPORTED, "decode supports Hq/Hkv in {1,2,4,8} (got %d)", G);
-  if (max_pages_per_seq <= 0 || num_pages <= 0)
-    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq and num_pages must be positive");
-  if (!q || !kcache || !vcache || !block_table || !seq_lens || !o)
-    return set_error(FA_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(o))
-    return set_error(FA_ERR_INVALID_ARG, "q, caches and o must be 16-byte aligned");
-  if (static_cast<long long>(max_pages_per_seq) * 16 > 0x7fffffffLL)
-    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq too large");
   int dev, rc;
+  if ((rc = validate_decode(q, kcache, vcache, block_table, seq_lens, o, B, Hq, Hkv, D, page_size,
+                            scale, max_pages_per_seq, num_pages)) != FA_OK)
+    return rc;
+  if (B == 0 || Hq == 0) return FA_OK;
   if ((rc = current_sm100(&dev)) != FA_OK) return rc;
   return launch_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
                        scale, max_pages_per_seq, num_pages, reinterpret_cast<cudaStream_t>(stream),
@@ -468,30 +861,11 @@ int fa_decode_paged_noalloc(const void* q, const void* kcache, const void* vcach
                             int Hq, int Hkv, int D, int page_size, float scale, fa_stream_t stream,
                             int max_pages_per_seq, int num_pages, float* lse) {
   using namespace fa;
-  if (B < 0 || Hq < 0 || Hkv < 0 || max_pages_per_seq < 0 || num_pages < 0)
-    return set_error(FA_ERR_INVALID_ARG, "negative size");
-  if (!(std::isfinite(scale) && scale > 0.f))
-    return set_error(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
-  if (D != 128) return set_error(FA_ERR_UNSUPPORTED, "decode supports D == 128 only (got %d)", D);
-  if (page_size != 16)
-    return set_error(FA_ERR_UNSUPPORTED, "decode supports page_size == 16 only (got %d)",
-                     page_size);
-  if (B == 0 || Hq == 0) return FA_OK;
-  if (Hkv <= 0 || Hq % Hkv != 0)
-    return set_error(FA_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d)", Hq,
-                     Hkv);
-  const int G = Hq / Hkv;
-  if (G != 1 && G != 2 && G != 4 && G != 8)
-    return set_error(FA_ERR_UNSUPPORTED, "decode supports Hq/Hkv in {1,2,4,8} (got %d)", G);
-  if (max_pages_per_seq <= 0 || num_pages <= 0)
-    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq and num_pages must be positive");
-  if (!q || !kcache || !vcache || !block_table || !seq_lens || !o)
-    return set_error(FA_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(o))
-    return set_error(FA_ERR_INVALID_ARG, "q, caches and o must be 16-byte aligned");
-  if (static_cast<long long>(max_pages_per_seq) * 16 > 0x7fffffffLL)
-    return set_error(FA_ERR_INVALID_ARG, "max_pages_per_seq too large");
   int dev, rc;
+  if ((rc = validate_decode(q, kcache, vcache, block_table, seq_lens, o, B, Hq, Hkv, D, page_size,
+                            scale, max_pages_per_seq, num_pages)) != FA_OK)
+    return rc;
+  if (B == 0 || Hq == 0) return FA_OK;
   // Problems that no schedule fits are rejected before the device is touched;
   // the plan for the device's SM count is checked again at launch.
   if ((rc = check_decode_noalloc(B, Hq, Hkv, max_pages_per_seq, 0)) != FA_OK) return rc;
@@ -532,8 +906,11 @@ int fa_device_status(void) {
   if (word & kErrDiverged)
     return set_error(FA_ERR_DEVICE_DIVERGED,
                      "a tensor-memory access found its warp diverged (word 0x%x)", word);
-  return set_error(FA_ERR_DEVICE_INDEX, "out-of-range block-table entry or length (word 0x%x)",
-                   word);
+  if (word & kErrBadIndex)
+    return set_error(FA_ERR_DEVICE_INDEX,
+                     "out-of-range block-table entry, length, position or slot (word 0x%x)", word);
+  return set_error(FA_ERR_DEVICE_NO_PAGES,
+                   "new tokens did not fit the free pages or the token rows (word 0x%x)", word);
 }
 
 void fa_release(void) {

@@ -100,6 +100,49 @@ void release_host_pipeline_resources();
 // One bounded wait that nothing satisfies, given up after limit_us (validated).
 int launch_wait_selftest(unsigned limit_us, int* gave_up, cudaStream_t stream, int device);
 
+// Per-head norm and rotation of q and k (validated arguments); slot_map != nullptr:
+// K and V go to the page pool [num_slots, Hkv, D] instead of k_out.
+struct NormRopeArgs {
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  long long q_stride = 0, k_stride = 0, v_stride = 0;   // elements between tokens
+  const void *q_weight = nullptr, *k_weight = nullptr;
+  const float* table = nullptr;
+  const int32_t* positions = nullptr;
+  const uint8_t* pair_axis = nullptr;
+  const int64_t* slot_map = nullptr;
+  void *q_out = nullptr, *k_out = nullptr, *v_out = nullptr;
+  long long num_slots = 0;
+  int T = 0, N = 0, Hq = 0, Hkv = 0, D = 0, rot_dim = 0, max_pos = 0, n_axes = 1;
+  bool interleaved = false, heads_first = false, bf16 = true;
+  float eps = 0.f;
+};
+struct NormRopeGrads {
+  const void *dq_out = nullptr, *dk_out = nullptr;
+  void *dq = nullptr, *dk = nullptr;
+  long long dq_stride = 0, dk_stride = 0;
+  float *dq_weight = nullptr, *dk_weight = nullptr, *scratch = nullptr;
+};
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream, int device);
+int launch_norm_rope_bwd(const NormRopeArgs& a, const NormRopeGrads& g, cudaStream_t stream,
+                         int device);
+
+// Block tables, positions and slots of a step's new tokens (validated arguments).
+struct ExtendArgs {
+  int32_t* block_table = nullptr;
+  const int32_t *seq_lens = nullptr, *new_lens = nullptr, *free_pages = nullptr,
+                *free_count = nullptr;
+  int32_t *seq_lens_out = nullptr, *free_count_out = nullptr, *cu_seqlens_q = nullptr,
+          *positions = nullptr;
+  int64_t* slot_map = nullptr;
+  int B = 0, max_pages_per_seq = 0, num_pages = 0, max_tokens = 0;
+};
+constexpr int kMaxExtendSeqs = 16384;   // three ints each in shared memory
+int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device);
+
+// Raises a kernel's dynamic shared-memory limit, once per device and context.
+enum SmemKernel : int { kSmemExtend = 0, kSmemKernels };
+int raise_smem_limit(const void* kernel, int bytes, int device, SmemKernel which);
+
 // Release cached per-device resources owned by the decode path.
 void release_decode_resources();
 

@@ -11,8 +11,9 @@ namespace fa {
 // Device-side error word, read and cleared by fa_device_status().
 // Bit 0: a bounded wait ran out; bit 1: an index read from device memory
 // (block table entry or sequence length) was out of range; bit 2 (debug builds
-// only): a warp-collective tensor-memory instruction found its warp diverged.
-enum : int { kErrTimeout = 1, kErrBadIndex = 2, kErrDiverged = 4 };
+// only): a warp-collective tensor-memory instruction found its warp diverged;
+// bit 3: new tokens did not fit (free pages or token rows).
+enum : int { kErrTimeout = 1, kErrBadIndex = 2, kErrDiverged = 4, kErrNoPages = 8 };
 
 // FA_DEBUG=1 builds check, before every tensor-memory load, store and their
 // waits (warp-collective tcgen05 instructions), that all 32 lanes of the warp

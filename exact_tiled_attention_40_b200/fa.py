@@ -19,15 +19,19 @@ LIB_PATH = os.environ.get("FA_LIBRARY") or os.path.join(HERE, "libfa_sm100.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "fa.h")
 
 FA_OK = 0
+QK_NORM_ROPE_SCRATCH_ROWS = 1024      # FA_QK_NORM_ROPE_SCRATCH_ROWS
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
           4: "FA_ERR_DEVICE_TIMEOUT", 5: "FA_ERR_DEVICE_INDEX", 6: "FA_ERR_NO_DEVICE",
-          7: "FA_ERR_DEVICE_DIVERGED"}
+          7: "FA_ERR_DEVICE_DIVERGED", 8: "FA_ERR_DEVICE_NO_PAGES"}
 
 _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
+_NORM_ROPE = [_P] * 9 + [_I] * 5 + [_L] * 2 + [_I] * 5 + [_F, _P]
+_NORM_ROPE_BWD = [_P] * 14 + [_I] * 5 + [_L] * 4 + [_I] * 5 + [_F, _P]
 _SIGS = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_fp16": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
@@ -46,6 +50,12 @@ _SIGS = {
     "fa_decode_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _I, _P]),
     "fa_decode_paged_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _I,
                                      _P]),
+    "fa_extend_pages": (_I, [_P] * 10 + [_I] * 5 + [_P]),
+    "fa_qk_norm_rope": (_I, _NORM_ROPE),
+    "fa_qk_norm_rope_fp16": (_I, _NORM_ROPE),
+    "fa_qk_norm_rope_bwd": (_I, _NORM_ROPE_BWD),
+    "fa_qk_norm_rope_bwd_fp16": (_I, _NORM_ROPE_BWD),
+    "fa_append_paged": (_I, [_P] * 12 + [_I] * 6 + [_L] * 3 + [_I] * 4 + [_F, _P]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_uint, _P, _P]),
     "fa_last_error_string": (ctypes.c_char_p, []),
     "fa_device_status": (_I, []),
@@ -93,6 +103,33 @@ def _ptr(t):
 
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on_current_device(where, *tensors):
+    """The kernels run on the current device: refuses tensors (None: absent) elsewhere."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            raise FAError(1, where, "tensors must live on the current CUDA device")
+
+
+def _dtypes(where, dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise FAError(1, where, f"{name} must be {str(dtype)[6:]}, not {str(t.dtype)[6:]}")
+
+
+def _shape(where, name, t, want):
+    """Refuses t unless its shape is `want` (None: any size)."""
+    if t.dim() != len(want) or any(w is not None and w != n for w, n in zip(want, t.shape)):
+        raise FAError(1, where, f"{name} must have shape {list(want)}, not {list(t.shape)}")
+
+
+def _aligned16(t):
+    """t (or None) contiguous and at a 16-byte boundary, copied where it is not."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def fa_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, causal, stream=None):
@@ -392,6 +429,230 @@ def decode_paged_noalloc(q, kcache, vcache, block_table, seq_lens, o, lse=None, 
                                          _ptr(seq_lens), _ptr(o), B, Hq, Hkv, D, page_size,
                                          float(scale), s, block_table.shape[1], num_pages,
                                          _ptr(lse)), "fa_decode_paged_noalloc")
+
+
+def fa_extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, seq_lens_out,
+                    free_count_out, cu_seqlens_q, positions, slot_map, B, max_pages_per_seq,
+                    num_pages, page_size, max_tokens, stream=None):
+    """Raw call of the C entry point."""
+    s = _stream(block_table.device) if stream is None else ctypes.c_void_p(stream)
+    _check(lib().fa_extend_pages(
+        _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), _ptr(free_pages), _ptr(free_count),
+        _ptr(seq_lens_out), _ptr(free_count_out), _ptr(cu_seqlens_q), _ptr(positions),
+        _ptr(slot_map), B, max_pages_per_seq, num_pages, page_size, max_tokens, s),
+        "fa_extend_pages")
+
+
+def extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, num_pages, max_tokens):
+    """Pages, positions and cache slots of a step's new tokens: block_table [B, max_pages]
+    (int32, contiguous) gets the new pages of every sequence in place, taken from the end
+    of the first free_count[0] entries of free_pages [num_pages].  Returns (seq_lens +
+    new_lens [B], cu_seqlens_q [B+1], positions [max_tokens] int32, slot_map [max_tokens]
+    int64, pages left [1])."""
+    where = "extend_pages"
+    _on_current_device(where, block_table, seq_lens, new_lens, free_pages, free_count)
+    _dtypes(where, torch.int32, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens,
+            free_pages=free_pages, free_count=free_count)
+    _shape(where, "block_table", block_table, (None, None))
+    B, max_pages = block_table.shape
+    _shape(where, "seq_lens", seq_lens, (B,))
+    _shape(where, "new_lens", new_lens, (B,))
+    _shape(where, "free_pages", free_pages, (num_pages,))
+    _shape(where, "free_count", free_count, (1,))
+    if not block_table.is_contiguous():
+        raise FAError(1, where, "block_table is written in place and must be contiguous")
+    dev = block_table.device
+    if max_tokens < 0:
+        raise FAError(1, where, "max_tokens must not be negative")
+    lens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    left = torch.empty(1, dtype=torch.int32, device=dev)
+    fa_extend_pages(block_table, seq_lens.contiguous(), new_lens.contiguous(),
+                    free_pages.contiguous(), free_count, lens_out, left, cu, positions, slots, B,
+                    max_pages, num_pages, 16, max_tokens)
+    return lens_out, cu, positions, slots, left
+
+
+def _head_rows(t):
+    """t [..., H, D] as the library reads token-major rows: t itself where each token's
+    heads are contiguous and one stride leads from token to token (a view of a QKV
+    projection), a contiguous copy otherwise; and that stride in elements."""
+    lead, (H, D), st = t.shape[:-2], t.shape[-2:], t.stride()
+    stride = H * D                              # no step from token to token: any will do
+    for n, s in zip(reversed(lead), reversed(st[:-2])):
+        if n > 1:
+            stride = s
+            break
+    span = 1
+    for n, s in zip(reversed(lead), reversed(st[:-2])):
+        if n > 1 and s != stride * span:
+            return _aligned16(t), H * D
+        span *= n
+    if (st[-1] == 1 and (H == 1 or st[-2] == D) and stride >= H * D and stride % 8 == 0
+            and t.data_ptr() % 16 == 0):
+        return t, stride
+    return _aligned16(t), H * D
+
+
+def _norm_rope_args(where, q, k, q_weight, k_weight, table, positions, pair_axis, lead):
+    """Checks shared by the norm + rotation calls; the leading sizes, heads and sizes of
+    the table, and contiguous weights, table, positions and axes."""
+    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise FAError(1, where, "q must be bf16 or fp16")
+    _dtypes(where, q.dtype, k=k, q_weight=q_weight, k_weight=k_weight)
+    _dtypes(where, torch.float32, table=table)
+    _dtypes(where, torch.int32, positions=positions)
+    _dtypes(where, torch.uint8, pair_axis=pair_axis)
+    _shape(where, "q", q, (None,) * (lead + 2))
+    D = q.shape[-1]
+    _shape(where, "k", k, tuple(q.shape[:lead]) + (None, D))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _shape(where, name, w, (D,))
+    _shape(where, "table", table, (None, None))
+    max_pos, rot = table.shape
+    tokens = 1
+    for n in q.shape[:lead]:
+        tokens *= n
+    if positions.dim() == 1:
+        positions = positions[None]
+    _shape(where, "positions", positions, (None, tokens))
+    axes = positions.shape[0]
+    if axes != 1:
+        if pair_axis is None:
+            raise FAError(1, where, "pair_axis is needed with more than one axis")
+        _shape(where, "pair_axis", pair_axis, (rot // 2,))
+        pair_axis = pair_axis.contiguous()
+    return (_aligned16(q_weight), _aligned16(k_weight), _aligned16(table), positions.contiguous(),
+            pair_axis, rot, max_pos, axes)
+
+
+def fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N, Hq,
+                    Hkv, D, q_stride, k_stride, rot_dim, max_positions, n_axes, interleaved,
+                    heads_first, eps, stream=None):
+    """Raw call of the C entry point (bf16 or fp16 chosen from q's dtype)."""
+    fn = lib().fa_qk_norm_rope if q.dtype == torch.bfloat16 else lib().fa_qk_norm_rope_fp16
+    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    _check(fn(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(table), _ptr(positions),
+              _ptr(pair_axis), _ptr(q_out), _ptr(k_out), B, N, Hq, Hkv, D, q_stride, k_stride,
+              rot_dim, max_positions, n_axes, int(bool(interleaved)), int(bool(heads_first)),
+              float(eps), s), "fa_qk_norm_rope")
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis=None, eps=1e-6,
+                 interleaved=False, heads_first=True):
+    """Per-head RMS norm (a weight of None: none) and rotary rotation of q [B, N, Hq, D] and
+    k [B, N, Hkv, D] (bf16 or fp16; views of one projection are read in place) by
+    table [max_positions, rot_dim] fp32 (cosines, then sines) at positions
+    [n_axes, B * N] (or [B * N]) int32, pair j along axis pair_axis[j] (uint8).
+    Returns q and k as [B, H, N, D] (heads_first, what `attention` takes) or [B, N, H, D]."""
+    where = "qk_norm_rope"
+    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
+        where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
+    B, N, Hq, D = q.shape
+    Hkv = k.shape[2]
+    q, q_stride = _head_rows(q)
+    k, k_stride = _head_rows(k)
+    shape = (lambda H: (B, H, N, D)) if heads_first else (lambda H: (B, N, H, D))
+    q_out = torch.empty(shape(Hq), dtype=q.dtype, device=q.device)
+    k_out = torch.empty(shape(Hkv), dtype=q.dtype, device=q.device)
+    fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N, Hq,
+                    Hkv, D, q_stride, k_stride, rot, max_pos, axes, interleaved, heads_first, eps)
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, table, positions, pair_axis, dq,
+                        dk, dq_weight, dk_weight, scratch, B, N, Hq, Hkv, D, q_stride, k_stride,
+                        dq_stride, dk_stride, rot_dim, max_positions, n_axes, interleaved,
+                        heads_first, eps, stream=None):
+    """Raw call of the C entry point (bf16 or fp16 chosen from q's dtype)."""
+    fn = lib().fa_qk_norm_rope_bwd if q.dtype == torch.bfloat16 else lib().fa_qk_norm_rope_bwd_fp16
+    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    _check(fn(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight),
+              _ptr(table), _ptr(positions), _ptr(pair_axis), _ptr(dq), _ptr(dk), _ptr(dq_weight),
+              _ptr(dk_weight), _ptr(scratch), B, N, Hq, Hkv, D, q_stride, k_stride, dq_stride,
+              dk_stride, rot_dim, max_positions, n_axes, int(bool(interleaved)),
+              int(bool(heads_first)), float(eps), s), "fa_qk_norm_rope_bwd")
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table, positions,
+                          pair_axis=None, eps=1e-6, interleaved=False, heads_first=True):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope for the gradients dq_out, dk_out of its
+    outputs: dq [B, N, Hq, D] and dk [B, N, Hkv, D] in q's dtype, the weights' in fp32
+    (None where the weight is None)."""
+    where = "qk_norm_rope_backward"
+    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
+        where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
+    _on_current_device(where, dq_out, dk_out)
+    _dtypes(where, q.dtype, dq_out=dq_out, dk_out=dk_out)
+    B, N, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _shape(where, "dq_out", dq_out, (B, Hq, N, D) if heads_first else (B, N, Hq, D))
+    _shape(where, "dk_out", dk_out, (B, Hkv, N, D) if heads_first else (B, N, Hkv, D))
+    q, q_stride = _head_rows(q)
+    k, k_stride = _head_rows(k)
+    dev = q.device
+    dq = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+    dk = torch.empty((B, N, Hkv, D), dtype=q.dtype, device=dev)
+    dwq = dwk = scratch = None
+    if q_weight is not None:
+        dwq = torch.empty(D, dtype=torch.float32, device=dev)
+    if k_weight is not None:
+        dwk = torch.empty(D, dtype=torch.float32, device=dev)
+    if q_weight is not None or k_weight is not None:
+        scratch = torch.empty(2 * QK_NORM_ROPE_SCRATCH_ROWS * D, dtype=torch.float32, device=dev)
+    fa_qk_norm_rope_bwd(q, k, _aligned16(dq_out), _aligned16(dk_out), q_weight, k_weight, table,
+                        positions, pair_axis, dq, dk, dwq, dwk, scratch, B, N, Hq, Hkv, D, q_stride,
+                        k_stride, Hq * D, Hkv * D, rot, max_pos, axes, interleaved, heads_first,
+                        eps)
+    return dq, dk, dwq, dwk
+
+
+def fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis, slot_map, q_out,
+                    kcache, vcache, T, Hq, Hkv, D, page_size, num_pages, q_stride, k_stride,
+                    v_stride, rot_dim, max_positions, n_axes, interleaved, eps, stream=None):
+    """Raw call of the C entry point (bf16)."""
+    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    _check(lib().fa_append_paged(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(table), _ptr(positions),
+        _ptr(pair_axis), _ptr(slot_map), _ptr(q_out), _ptr(kcache), _ptr(vcache), T, Hq, Hkv, D,
+        page_size, num_pages, q_stride, k_stride, v_stride, rot_dim, max_positions, n_axes,
+        int(bool(interleaved)), float(eps), s), "fa_append_paged")
+
+
+def append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table, positions,
+                 pair_axis=None, eps=1e-6, interleaved=False):
+    """qk_norm_rope for the new tokens of a serving step: q [T, Hq, D], k, v [T, Hkv, D] (bf16)
+    at slots slot_map [T] (int64, as extend_pages returns them; negative: padding) of the page
+    pool kcache, vcache [num_pages, 16, Hkv, D], where K (normed and rotated) and V are written
+    in place.  Returns q [T, Hq, D] for prefill_paged and the decode calls; rows of padding
+    tokens are left unset."""
+    where = "append_paged"
+    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
+        where, q, k, q_weight, k_weight, table, positions, pair_axis, 1)
+    _on_current_device(where, v, kcache, vcache, slot_map)
+    _dtypes(where, torch.bfloat16, q=q, v=v, kcache=kcache, vcache=vcache)
+    _dtypes(where, torch.int64, slot_map=slot_map)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    _shape(where, "v", v, (T, Hkv, D))
+    _shape(where, "kcache", kcache, (None, None, Hkv, D))
+    _shape(where, "vcache", vcache, tuple(kcache.shape))
+    _shape(where, "slot_map", slot_map, (T,))
+    if not (kcache.is_contiguous() and vcache.is_contiguous()):
+        raise FAError(1, where, "the caches are written in place and must be contiguous")
+    q, q_stride = _head_rows(q)
+    k, k_stride = _head_rows(k)
+    v, v_stride = _head_rows(v)
+    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis,
+                    slot_map.contiguous(), q_out, kcache, vcache, T, Hq, Hkv, D, kcache.shape[1],
+                    kcache.shape[0], q_stride, k_stride, v_stride, rot, max_pos, axes, interleaved,
+                    eps)
+    return q_out
 
 
 def device_status() -> int:

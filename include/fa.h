@@ -50,8 +50,10 @@ enum fa_status {
   FA_ERR_DEVICE_TIMEOUT = 4, /* fa_device_status(): a bounded in-kernel wait ran out */
   FA_ERR_DEVICE_INDEX = 5,   /* fa_device_status(): a block-table entry or length was out of range */
   FA_ERR_NO_DEVICE = 6,      /* no sm_100 device is current */
-  FA_ERR_DEVICE_DIVERGED = 7 /* fa_device_status(), FA_DEBUG builds only: a tensor-memory
-                                load/store found its warp diverged and was skipped */
+  FA_ERR_DEVICE_DIVERGED = 7, /* fa_device_status(), FA_DEBUG builds only: a tensor-memory
+                                 load/store found its warp diverged and was skipped */
+  FA_ERR_DEVICE_NO_PAGES = 8 /* fa_device_status(): fa_extend_pages ran out of free pages or of
+                                token rows and left sequences as they were */
 };
 
 /*
@@ -326,14 +328,143 @@ int fa_decode_paged_noalloc(const void* q, const void* kcache, const void* vcach
                             int Hq, int Hkv, int D, int page_size, float scale,
                             fa_stream_t stream, int max_pages_per_seq, int num_pages, float* lse);
 
+/*
+ * Block tables, positions and cache slots of one step's new tokens, from request
+ * lengths and a list of free pages, all on the device.
+ *   seq_lens, new_lens  [B] int32: tokens in the cache and tokens to add (0 or more)
+ *   free_pages   [num_pages] int32, free_count [1] int32: the first free_count[0]
+ *                entries are free page ids; they are taken from the end
+ *   block_table  [B, max_pages_per_seq] int32 (new entries written): sequence b gets
+ *                ceil((seq_lens[b] + new_lens[b]) / 16) - ceil(seq_lens[b] / 16) pages
+ *                behind those it has, sequences in order
+ *   seq_lens_out [B] int32 (written): seq_lens + new_lens; may be seq_lens itself
+ *   free_count_out [1] int32 (written): pages left; may be free_count itself
+ *   cu_seqlens_q [B + 1] int32 (written): prefix sums of the tokens added
+ *   positions    [max_tokens] int32, slot_map [max_tokens] int64 (written): row
+ *                cu_seqlens_q[b] + i is token i of sequence b, at position
+ *                seq_lens[b] + i and in slot 16 * page + offset of the pool; rows
+ *                behind the last token get position 0 and slot -1
+ * The outputs are the cu_seqlens_q, seq_lens and slots that fa_append_paged,
+ * fa_fwd_paged and the decode entry points read.  Other than the two arrays named,
+ * outputs must not overlap inputs.  To give pages back, write their ids to
+ * free_pages from entry free_count[0] on and raise free_count[0].
+ * A sequence with a negative length, or longer than its block_table row, stays as it
+ * is and raises FA_ERR_DEVICE_INDEX, as do page ids outside [0, num_pages) (their
+ * tokens get slot -1) and a free_count outside [0, num_pages] (which counts as 0).
+ * From the first sequence on whose pages or tokens do not fit free_count or
+ * max_tokens, sequences stay as they are and FA_ERR_DEVICE_NO_PAGES is raised.
+ * B <= 16384; page_size == 16.  One launch; nothing is allocated.
+ */
+int fa_extend_pages(int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
+                    const int32_t* free_pages, const int32_t* free_count, int32_t* seq_lens_out,
+                    int32_t* free_count_out, int32_t* cu_seqlens_q, int32_t* positions,
+                    int64_t* slot_map, int B, int max_pages_per_seq, int num_pages, int page_size,
+                    int max_tokens, fa_stream_t stream);
+
+/*
+ * Per-head RMS norm and rotary position rotation of queries and keys in one pass
+ * (bf16), before attention.  For a head row x of token t:
+ *     y = R_t (w * x / sqrt(mean(x^2) + eps)),
+ * R_t turning element pair j of the first rot_dim elements by the angle whose cosine
+ * and sine are table[p][j] and table[p][rot_dim / 2 + j], p the token's position.
+ *   q [B, N, Hq, D], k [B, N, Hkv, D] bf16: token-major rows with q_stride and k_stride
+ *       elements between tokens (multiples of 8), so they may be views of one QKV
+ *       projection; each token's heads are contiguous
+ *   q_weight, k_weight  [D] bf16, or NULL: that tensor is not normalised
+ *   table      [max_positions, rot_dim] fp32
+ *   positions  [n_axes, B * N] int32; pair_axis [rot_dim / 2] uint8: pair j takes its
+ *       position from axis pair_axis[j] (time, height, width of image and video
+ *       tokens); with n_axes == 1 pair_axis is not read and may be NULL
+ *   q_out, k_out  (written) bf16, contiguous: [B, N, H, D], or with heads_first
+ *       [B, H, N, D], the layout of fa_fwd
+ * interleaved == 0: pair j is elements (j, j + rot_dim / 2); otherwise (2j, 2j + 1).
+ * D in {64, 128}; rot_dim a multiple of 16 in [0, D] (0: no rotation, table and
+ * positions are not read); elements from rot_dim on are not turned.  1 <= n_axes <= 8.
+ * Hq or Hkv may be 0.  Computed in fp32 and rounded once.  Positions outside
+ * [0, max_positions) and axes outside [0, n_axes) raise FA_ERR_DEVICE_INDEX and count
+ * as 0.  Outputs must not overlap the inputs.  16-byte alignment of all tensors.
+ */
+int fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                    const float* table, const int32_t* positions, const uint8_t* pair_axis,
+                    void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int D,
+                    long long q_stride, long long k_stride, int rot_dim, int max_positions,
+                    int n_axes, int interleaved, int heads_first, float eps, fa_stream_t stream);
+
+/* Same as fa_qk_norm_rope with fp16 tensors and weights. */
+int fa_qk_norm_rope_fp16(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                         const float* table, const int32_t* positions, const uint8_t* pair_axis,
+                         void* q_out, void* k_out, int B, int N, int Hq, int Hkv, int D,
+                         long long q_stride, long long k_stride, int rot_dim, int max_positions,
+                         int n_axes, int interleaved, int heads_first, float eps,
+                         fa_stream_t stream);
+
+/*
+ * Backward pass of fa_qk_norm_rope (bf16): with g = R_t^T dy and
+ * xhat = x / sqrt(mean(x^2) + eps),
+ *     dw = sum over rows of g * xhat,
+ *     dx = (w * g - xhat * mean(w * g * xhat)) / sqrt(mean(x^2) + eps).
+ *   q, k, weights, table, positions, pair_axis: the forward's inputs
+ *   dq_out, dk_out  gradients of its outputs, in the outputs' layout (fa_bwd's dq and
+ *       dk with heads_first)
+ *   dq, dk   (written) bf16 [B, N, H, D], dq_stride and dk_stride elements between
+ *       tokens (they may be views of one gradient of the projection)
+ *   dq_weight, dk_weight  [D] fp32 (written where the weight is given)
+ *   scratch  [2 * FA_QK_NORM_ROPE_SCRATCH_ROWS * D] fp32, caller-provided; not needed
+ *       without weights
+ * No atomics: the same inputs give the same bits on the same device.
+ */
+#define FA_QK_NORM_ROPE_SCRATCH_ROWS 1024
+int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                        const void* q_weight, const void* k_weight, const float* table,
+                        const int32_t* positions, const uint8_t* pair_axis, void* dq, void* dk,
+                        float* dq_weight, float* dk_weight, float* scratch, int B, int N, int Hq,
+                        int Hkv, int D, long long q_stride, long long k_stride,
+                        long long dq_stride, long long dk_stride, int rot_dim, int max_positions,
+                        int n_axes, int interleaved, int heads_first, float eps,
+                        fa_stream_t stream);
+
+/* Same as fa_qk_norm_rope_bwd with fp16 tensors and weights (fp32 dq_weight, dk_weight). */
+int fa_qk_norm_rope_bwd_fp16(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                             const void* q_weight, const void* k_weight, const float* table,
+                             const int32_t* positions, const uint8_t* pair_axis, void* dq,
+                             void* dk, float* dq_weight, float* dk_weight, float* scratch, int B,
+                             int N, int Hq, int Hkv, int D, long long q_stride,
+                             long long k_stride, long long dq_stride, long long dk_stride,
+                             int rot_dim, int max_positions, int n_axes, int interleaved,
+                             int heads_first, float eps, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope for the new tokens of a serving step, with K and V written to the
+ * page pool (bf16): q_out [T, Hq, D] is what fa_fwd_paged and the decode entry points
+ * read, and token t's keys and values go to slot slot_map[t] of
+ * kcache, vcache [num_pages, 16, Hkv, D] (slot 16 * page + offset), V copied as it is.
+ *   q [T, Hq, D], k, v [T, Hkv, D] with q_stride, k_stride, v_stride elements between
+ *       tokens; the other arguments as for fa_qk_norm_rope with B * N = T
+ *   slot_map  [T] int64, as fa_extend_pages writes it.  A negative slot marks a padding
+ *       row, of which nothing is read but the slot and nothing is written, q_out
+ *       included; a slot beyond the pool raises FA_ERR_DEVICE_INDEX and is treated
+ *       alike.  Slots must be distinct: one that is given twice holds a mixture.
+ * The attention entry points read whole pages: fa_fwd_paged needs finite numbers in
+ * the slots of a sequence's last page that are not written yet, so clear the pool once
+ * when it is allocated.
+ */
+int fa_append_paged(const void* q, const void* k, const void* v, const void* q_weight,
+                    const void* k_weight, const float* table, const int32_t* positions,
+                    const uint8_t* pair_axis, const int64_t* slot_map, void* q_out, void* kcache,
+                    void* vcache, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
+                    long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                    int max_positions, int n_axes, int interleaved, float eps,
+                    fa_stream_t stream);
+
 /* Description of the last error returned on this thread ("" if none). */
 const char* fa_last_error_string(void);
 
 /*
  * Synchronises the current device, then reads and clears its device error
  * word.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_DEVICE_INDEX,
- * FA_ERR_DEVICE_DIVERGED (FA_DEBUG builds) or FA_ERR_CUDA; when several bits
- * are set the first of timeout, divergence, index is reported.
+ * FA_ERR_DEVICE_DIVERGED (FA_DEBUG builds), FA_ERR_DEVICE_NO_PAGES or
+ * FA_ERR_CUDA; when several bits are set the first of timeout, divergence,
+ * index, pages is reported.
  */
 int fa_device_status(void);
 

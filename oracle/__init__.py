@@ -17,3 +17,9 @@ from .attention_fp64 import (  # noqa: F401
     softmax_rows,
     varlen_attention,
 )
+from .step_fp64 import (  # noqa: F401
+    extend_pages,
+    norm_rope,
+    norm_rope_backward,
+    rotation,
+)
