@@ -856,6 +856,38 @@ int fa_decode_paged(const void* q, const void* kcache, const void* vcache,
                        dev);
 }
 
+int fa_decode_shared_prefix(const void* q, const void* kcache, const void* vcache,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* prefix_table, const int32_t* prefix_pages, void* o,
+                            int B, int Hq, int Hkv, int D, int page_size, float scale,
+                            fa_stream_t stream, int max_pages_per_seq, int max_prefix_pages,
+                            int num_pages, float* lse) {
+  using namespace fa;
+  int dev, rc;
+  if ((rc = validate_decode(q, kcache, vcache, block_table, seq_lens, o, B, Hq, Hkv, D, page_size,
+                            scale, max_pages_per_seq, num_pages)) != FA_OK)
+    return rc;
+  if (max_prefix_pages < 0) return set_error(FA_ERR_INVALID_ARG, "negative size");
+  if (B == 0 || Hq == 0) return FA_OK;
+  if (max_prefix_pages > max_pages_per_seq)
+    return set_error(FA_ERR_INVALID_ARG, "max_prefix_pages (%d) above max_pages_per_seq (%d)",
+                     max_prefix_pages, max_pages_per_seq);
+  if (num_pages >= 0x7fffffff / 16)
+    return set_error(FA_ERR_INVALID_ARG, "num_pages too large");
+  if (max_prefix_pages > 0 && (!prefix_table || !prefix_pages))
+    return set_error(FA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(prefix_table, 4) || !aligned(prefix_pages, 4))
+    return set_error(FA_ERR_INVALID_ARG, "prefix_table and prefix_pages must be 4-byte aligned");
+  if ((rc = current_sm100(&dev)) != FA_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (max_prefix_pages == 0)     // nothing can be shared
+    return launch_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, D,
+                         page_size, scale, max_pages_per_seq, num_pages, st, dev);
+  return launch_decode_shared(q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages,
+                              max_prefix_pages, o, lse, B, Hq, Hkv, scale, max_pages_per_seq,
+                              num_pages, st, dev);
+}
+
 int fa_decode_paged_noalloc(const void* q, const void* kcache, const void* vcache,
                             const int32_t* block_table, const int32_t* seq_lens, void* o, int B,
                             int Hq, int Hkv, int D, int page_size, float scale, fa_stream_t stream,

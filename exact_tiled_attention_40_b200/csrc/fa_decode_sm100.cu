@@ -31,6 +31,11 @@
 //    merge kernel combines each sequence's segments.
 //  * otherwise (direct): grid (chunk, sequence) of fixed page chunks, cache read
 //    straight from HBM with 16-byte non-allocating loads.
+//
+// SHARED instantiations serve batches whose sequences share their first pages: the
+// shared keys are the business of fa_prefix_sm100.cu, the kernels here stream each
+// sequence's own keys behind them, and the merge joins both.  A sequence shorter than
+// the shared pages does not take part: all of its keys are streamed as its own.
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
@@ -38,6 +43,7 @@
 #include <vector>
 
 #include "fa_internal.h"
+#include "prefix_split.cuh"
 #include "ptx_sm100.cuh"
 #include "../../include/fa.h"
 
@@ -96,6 +102,9 @@ struct DecodeParams {
   int hb_in_smem;              // streamed: the producer copies hb to shared memory
   float scale_log2;
   int* err;
+  PrefixWork pw;               // SHARED: the shared pages and how their work is split
+  const float* pre_o;          // SHARED: segments' partial outputs [slot][256][128]
+  const float* pre_lse;        // SHARED: their LSE [slot][256]
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -121,6 +130,23 @@ __device__ __forceinline__ int checked_len(const DecodeParams& p, int b) {
   return len;
 }
 
+// The keys that sequence b does not share: their number (-1: invalid length) and the
+// block-table entry they start at; `shared` is the batch's number of shared pages.
+struct OwnKeys {
+  int len, page0;
+};
+template <bool SHARED>
+__device__ __forceinline__ OwnKeys own_keys(int len, int shared) {
+  OwnKeys k;
+  k.len = len;
+  k.page0 = 0;
+  if (SHARED && len >= shared * kPage) {
+    k.len -= shared * kPage;
+    k.page0 = shared;
+  }
+  return k;
+}
+
 // Fold G partial sums held by 16 lanes (lane bits 0-3 = sub) into one full sum
 // per lane: lane `sub` ends with the total of head sub >> (4 - log2 G).
 template <int G>
@@ -144,7 +170,7 @@ __device__ __forceinline__ float fold_heads(float (&v)[G], int sub) {
   return x;
 }
 
-template <int G>
+template <int G, bool SHARED>
 __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const DecodeParams p) {
   constexpr int LG = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   constexpr int SHIFT = 4 - LG;       // lane `h << SHIFT` holds head h after the fold
@@ -159,11 +185,13 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
   const int sub = lane & 15;
   const int my_head = sub >> SHIFT;
 
-  const int len = checked_len(p, b);
-  if (len < 0) {
+  const int seq_len = checked_len(p, b);
+  if (seq_len < 0) {
     if (threadIdx.x == 0 && split == 0) atomicOr(p.err, kErrBadIndex);
     return;
   }
+  const OwnKeys mine = own_keys<SHARED>(seq_len, SHARED ? shared_pages(p.pw) : 0);
+  const int len = mine.len;
   const int npages = (len + kPage - 1) / kPage;
   const int pbeg = split * p.pps;
   if (pbeg >= npages) return;
@@ -192,7 +220,7 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
     float m_mine = -INFINITY;
 
     for (int pg = pbeg; pg < pend; ++pg) {
-      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + pg];
+      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + mine.page0 + pg];
       if (page < 0 || page >= p.num_pages) {
         if (lane == 0) atomicOr(p.err, kErrBadIndex);
         continue;
@@ -305,9 +333,12 @@ __host__ __device__ constexpr int box_bytes(int Hkv) { return Hkv * kHalf * 64 *
 __host__ __device__ constexpr int stage_kv_bytes(int Hkv) { return 2 * box_bytes(Hkv); }
 
 // hb[b] = sum over b' < b of ceil(len_b' / 8); hb[B] = total.  One block.
+// (SHARED: of the lengths without the shared keys.)
+template <bool SHARED>
 __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams p) {
   __shared__ int warp_sums[32];
   __shared__ int carry;
+  const int shared = SHARED ? shared_pages(p.pw) : 0;
   pdl_launch_dependents();   // the stream kernel may launch now; it waits for hb itself
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -323,7 +354,7 @@ __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams
       if (len < 0)
         atomicOr(p.err, kErrBadIndex);
       else
-        v = (len + kHalf - 1) / kHalf;
+        v = (own_keys<SHARED>(len, shared).len + kHalf - 1) / kHalf;
     }
     int x = v;   // inclusive warp scan
 #pragma unroll
@@ -350,22 +381,6 @@ __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams
     __syncthreads();
   }
   if (threadIdx.x == 0) p.hb[p.B] = carry;
-}
-
-// CTA whose share [c*H/C, (c+1)*H/C) holds half-page x < H: the largest c with
-// c*H/C <= x.
-__device__ __forceinline__ int cta_of(long long x, long long H, long long C) {
-  if ((x + 1) * C <= 0x7fffffffLL)             // the usual case: 32-bit division
-    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(C) - 1u) /
-                            static_cast<uint32_t>(H));
-  return static_cast<int>(((x + 1) * C - 1) / H);
-}
-// floor(c * H / C) for 0 <= c <= C
-__device__ __forceinline__ int share_edge(int c, int H, int C) {
-  const long long prod = static_cast<long long>(c) * H;
-  if (prod <= 0x7fffffffLL)
-    return static_cast<int>(static_cast<uint32_t>(prod) / static_cast<uint32_t>(C));
-  return static_cast<int>(prod / C);
 }
 
 // Share of CTA c: [x0, x1) = [c*H/C, (c+1)*H/C); its own part [x0, y) and its
@@ -407,7 +422,7 @@ struct StageMeta {
   int slot0;               // partial slot of this segment = slot0 + b
 };
 
-template <int G>
+template <int G, bool SHARED>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     fa_decode_stream_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const DecodeParams p) {
@@ -442,11 +457,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     fence_barrier_init();
   }
   // Everything above overlaps the scan kernel; the half-page offsets are its output.
-  pdl_wait();
+  // SHARED: the shared-prefix kernel stands in between and lets this one launch only
+  // after the scan has finished; its own output is not read here, so this grid starts
+  // on every SM that one has left and waits for it at the very end.
+  if constexpr (!SHARED) pdl_wait();
   // The merge kernel may launch once every CTA is past this point, so its launch
   // implies that the scan has finished: it reads the offsets before its own wait.
   pdl_launch_dependents();
-  const int H = p.hb[p.B];
+  const int shared = SHARED ? shared_pages(p.pw) : 0;
+  const int H = SHARED ? __ldcg(p.hb + p.B) : p.hb[p.B];
   const StreamSplit sp = stream_split(H, C, p.dyn_units_cap);
   const Share own = share_of(c, H, C, sp);
   __syncthreads();
@@ -460,7 +479,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const int* hbp = p.hb;
     if (p.hb_in_smem) {
       int* hb_sm = reinterpret_cast<int*>(dsm_raw + (sbase - smem_u32(dsm_raw)) + NS * 2 * SKV);
-      for (int i = lane; i <= p.B; i += 32) hb_sm[i] = p.hb[i];
+      for (int i = lane; i <= p.B; i += 32) hb_sm[i] = __ldcg(p.hb + i);
       __syncwarp();
       hbp = hb_sm;
     }
@@ -488,8 +507,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           bq = lo;
           const int hb_b = hbp[bq], hb_n = hbp[bq + 1];
           hh = x - hb_b;
-          page = p.block_table[static_cast<size_t>(bq) * p.max_pages + (hh >> 1)];
-          len = p.seq_lens[bq];
+          const OwnKeys mine = own_keys<SHARED>(p.seq_lens[bq], shared);
+          page = p.block_table[static_cast<size_t>(bq) * p.max_pages + mine.page0 + (hh >> 1)];
+          len = mine.len;
           const bool valid = page >= 0 && page < p.num_pages;
           flags = ((i == 0 || hh == 0) ? 1 : 0) | ((i == cnt - 1 || x + 1 == hb_n) ? 2 : 0) |
                   (valid ? 4 : 0);
@@ -561,6 +581,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       volatile int no_abort = 0;
       for (int i = max(0, issued - NS); i < issued; ++i)
         mbar_wait(full(i % NS), (i / NS) & 1, &no_abort, p.err, kWaitLimitNs);
+      // this grid may only complete after the shared-prefix kernel: the merge waits for
+      // this grid and then reads the partials of both
+      if constexpr (SHARED) pdl_wait();
     }
     return;
   }
@@ -641,10 +664,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           o[nn][0] *= alpha;
           o[nn][1] *= alpha;
         }
+        // slots behind the sequence's last token hold whatever the pool held: their
+        // weights are zero, and so must their values be (zero times NaN is NaN)
+        const uint32_t v_keep = (t0 < ntok ? 0x0000ffffu : 0u) | (t0 + 1 < ntok ? 0xffff0000u : 0u);
 #pragma unroll
         for (int ng = 0; ng < 4; ++ng) {
           uint32_t v0, v1, v2, v3;
           ldsm_x4_t(vaddr + ld_off[ng], v0, v1, v2, v3);
+          if (ntok < kHalf) {
+            v0 &= v_keep;
+            v1 &= v_keep;
+            v2 &= v_keep;
+            v3 &= v_keep;
+          }
           mma_bf16_1688(o[4 * ng + 0], pa, 0u, v0);
           mma_bf16_1688(o[4 * ng + 1], pa, 0u, v1);
           mma_bf16_1688(o[4 * ng + 2], pa, 0u, v2);
@@ -686,6 +718,82 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // kMergeBatch partial rows of a head in one round of independent loads.
 constexpr int kMergeBatch = 8;
 
+// Joins n partial results of one (sequence, query head) by their LSE: lse_at(k) and
+// row_at(k) (the lane's four columns) give the k-th.  32 partials at a time (one
+// sequence rarely has more): one LSE per lane and the first kMergeBatch rows load
+// together; a later chunk with a larger maximum rescales what is accumulated so far.
+template <class LseAt, class RowAt>
+__device__ __forceinline__ void merge_head(int n, int lane, LseAt lse_at, RowAt row_at,
+                                           uint16_t* o, float* lse) {
+  float wsum = 0.f, mx = -INFINITY;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int cnt = min(32, n - k0);
+    const float ls = lane < cnt ? lse_at(k0 + lane) : -INFINITY;
+    float4 v[kMergeBatch];
+#pragma unroll
+    for (int j = 0; j < kMergeBatch; ++j)
+      if (j < cnt) v[j] = row_at(k0 + j);
+    float m = ls;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = fmaxf(m, mx);
+    if (m == -INFINITY) continue;              // every LSE so far is -inf (warp-uniform)
+    const float sc = ex2((mx - m) * kLog2e);   // 0 on the first finite chunk
+    acc.x *= sc;
+    acc.y *= sc;
+    acc.z *= sc;
+    acc.w *= sc;
+    wsum *= sc;
+    mx = m;
+    const float w = (ls == -INFINITY) ? 0.f : ex2((ls - mx) * kLog2e);
+    wsum += w;
+    for (int j0 = 0; j0 < cnt; j0 += kMergeBatch) {
+      if (j0 > 0) {
+#pragma unroll
+        for (int j = 0; j < kMergeBatch; ++j)
+          if (j0 + j < cnt) v[j] = row_at(k0 + j0 + j);
+      }
+#pragma unroll
+      for (int j = 0; j < kMergeBatch; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        if (j0 + j < cnt) {
+          acc.x = fmaf(wj, v[j].x, acc.x);
+          acc.y = fmaf(wj, v[j].y, acc.y);
+          acc.z = fmaf(wj, v[j].z, acc.z);
+          acc.w = fmaf(wj, v[j].w, acc.w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  *reinterpret_cast<uint2*>(o + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lse && lane == 0) *lse = wsum > 0.f ? mx + __log2f(wsum) * kLn2 : -INFINITY;
+}
+
+// The segments of the shared prefix that hold row (b, h): n of them, the k-th at row
+// row0 + 256 k of the segments' workspace.
+struct PrefixRows {
+  int n;
+  size_t row0;
+};
+__device__ __forceinline__ PrefixRows prefix_rows(const DecodeParams& p, const PrefixSplit& sp,
+                                                  int b, int h) {
+  const int G = p.Hq / p.Hkv;
+  const int row = b * G + h % G;
+  const int item = (h / G) * p.pw.pairs + (row >> 8);
+  const int c0 = cta_of(static_cast<long long>(item) * sp.nt, sp.units, sp.ctas);
+  const int c1 = cta_of(static_cast<long long>(item + 1) * sp.nt - 1, sp.units, sp.ctas);
+  PrefixRows r;
+  r.n = c1 - c0 + 1;
+  r.row0 = static_cast<size_t>(c0 + item) * 256 + (row & 255);
+  return r;
+}
+
+template <bool SHARED>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kernel(
     const DecodeParams p) {
   __shared__ int slots[kMaxMergeSlots];
@@ -694,7 +802,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int xs = __ldcg(p.hb + b), xe = __ldcg(p.hb + b + 1);
-  if (xe <= xs) {                              // no keys (or an invalid length): O = 0, LSE = -inf
+  PrefixSplit ps;
+  bool sees = false;                           // the sequence has the shared keys
+  if constexpr (SHARED) {
+    ps = prefix_split(p.pw, p.pw.ctas);
+    sees = ps.pages > 0 && checked_len(p, b) >= ps.pages * kPage;
+  }
+  if (xe <= xs && !sees) {                     // no keys (or an invalid length): O = 0, LSE = -inf
     pdl_wait();
     for (int h = warp; h < p.Hq; h += kMergeWarps) {
       const size_t wid = static_cast<size_t>(b) * p.Hq + h;
@@ -707,8 +821,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
   const int C = p.nctas;
   const StreamSplit sp = stream_split(H, C, p.dyn_units_cap);
   if (warp == 0) {
-    const int c_first = cta_of(xs, H, C), c_last = cta_of(xe - 1, H, C);
     int base = 0;
+    // no own keys: an empty range
+    const int c_first = xe > xs ? cta_of(xs, H, C) : 0;
+    const int c_last = xe > xs ? cta_of(xe - 1, H, C) : -1;
     for (int c0 = c_first; c0 <= c_last; c0 += 32) {
       const int cc = c0 + lane;
       Share sh;
@@ -742,64 +858,60 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
   const int ns = n_slots_sm;
   pdl_wait();                                  // the stream kernel's partials
   const float4* wo = reinterpret_cast<const float4*>(p.ws_o);
-  auto row = [&](int k, int h) {               // lane's four columns of slot k, head h
-    return __ldcg(wo + (static_cast<size_t>(slots[k]) * p.Hq + h) * (kDecD / 4) + lane);
-  };
+  const float4* po = reinterpret_cast<const float4*>(p.pre_o);
   for (int h = warp; h < p.Hq; h += kMergeWarps) {
-    // 32 slots at a time (one sequence rarely has more): one LSE per lane and the
-    // first kMergeBatch rows load together; a later chunk with a larger maximum
-    // rescales what is accumulated so far
-    float wsum = 0.f, mx = -INFINITY;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < ns; k0 += 32) {
-      const int cnt = min(32, ns - k0);
-      const float ls =
-          lane < cnt ? __ldcg(p.ws_lse + static_cast<size_t>(slots[k0 + lane]) * p.Hq + h)
-                     : -INFINITY;
-      float4 v[kMergeBatch];
-#pragma unroll
-      for (int j = 0; j < kMergeBatch; ++j)
-        if (j < cnt) v[j] = row(k0 + j, h);
-      float m = ls;
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      m = fmaxf(m, mx);
-      if (m == -INFINITY) continue;            // every LSE so far is -inf (warp-uniform)
-      const float sc = ex2((mx - m) * kLog2e); // 0 on the first finite chunk
-      acc.x *= sc;
-      acc.y *= sc;
-      acc.z *= sc;
-      acc.w *= sc;
-      wsum *= sc;
-      mx = m;
-      const float w = (ls == -INFINITY) ? 0.f : ex2((ls - mx) * kLog2e);
-      wsum += w;
-      for (int j0 = 0; j0 < cnt; j0 += kMergeBatch) {
-        if (j0 > 0) {
-#pragma unroll
-          for (int j = 0; j < kMergeBatch; ++j)
-            if (j0 + j < cnt) v[j] = row(k0 + j0 + j, h);
-        }
-#pragma unroll
-        for (int j = 0; j < kMergeBatch; ++j) {
-          const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-          if (j0 + j < cnt) {
-            acc.x = fmaf(wj, v[j].x, acc.x);
-            acc.y = fmaf(wj, v[j].y, acc.y);
-            acc.z = fmaf(wj, v[j].z, acc.z);
-            acc.w = fmaf(wj, v[j].w, acc.w);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
+    PrefixRows pr;
+    pr.n = 0;
+    pr.row0 = 0;
+    if (SHARED && sees) pr = prefix_rows(p, ps, b, h);
     const size_t wid = static_cast<size_t>(b) * p.Hq + h;
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    *reinterpret_cast<uint2*>(p.o + wid * kDecD + lane * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (p.lse && lane == 0) p.lse[wid] = wsum > 0.f ? mx + __log2f(wsum) * kLn2 : -INFINITY;
+    merge_head(
+        ns + pr.n, lane,
+        [&](int k) {
+          if (SHARED && k >= ns) return __ldcg(p.pre_lse + pr.row0 + static_cast<size_t>(k - ns) * 256);
+          return __ldcg(p.ws_lse + static_cast<size_t>(slots[k]) * p.Hq + h);
+        },
+        [&](int k) {
+          if (SHARED && k >= ns)
+            return __ldcg(po + (pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane);
+          return __ldcg(wo + (static_cast<size_t>(slots[k]) * p.Hq + h) * (kDecD / 4) + lane);
+        },
+        p.o + wid * kDecD, p.lse ? p.lse + wid : nullptr);
   }
+}
+
+// SHARED, direct schedule: joins the chunks of a sequence's own keys and the segments of
+// the shared prefix; a warp per (sequence, query head).
+__global__ void __launch_bounds__(kDecThreads) fa_decode_shared_combine_kernel(
+    const DecodeParams p) {
+  const long long bh = static_cast<long long>(blockIdx.x) * kDecWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (bh >= static_cast<long long>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(bh / p.Hq);
+  const int h = static_cast<int>(bh - static_cast<long long>(b) * p.Hq);
+  const PrefixSplit ps = prefix_split(p.pw, p.pw.ctas);
+  const int seq_len = checked_len(p, b);
+  const int len = own_keys<true>(seq_len, ps.pages).len;
+  const int npages = len > 0 ? (len + kPage - 1) / kPage : 0;
+  const int ns = (npages + p.pps - 1) / p.pps;
+  PrefixRows pr;
+  pr.n = 0;
+  pr.row0 = 0;
+  if (ps.pages > 0 && seq_len >= ps.pages * kPage) pr = prefix_rows(p, ps, b, h);
+  const float4* wo = reinterpret_cast<const float4*>(p.ws_o);
+  const float4* po = reinterpret_cast<const float4*>(p.pre_o);
+  const size_t base = static_cast<size_t>(b) * p.nsplit * p.Hq + h;
+  merge_head(
+      ns + pr.n, lane,
+      [&](int k) {
+        return k >= ns ? p.pre_lse[pr.row0 + static_cast<size_t>(k - ns) * 256]
+                       : p.ws_lse[base + static_cast<size_t>(k) * p.Hq];
+      },
+      [&](int k) {
+        return k >= ns ? po[(pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane]
+                       : wo[(base + static_cast<size_t>(k) * p.Hq) * (kDecD / 4) + lane];
+      },
+      p.o + bh * kDecD, p.lse ? p.lse + bh : nullptr);
 }
 
 // One CTA of 128 threads per (sequence, query head); thread d owns output column d.
@@ -873,6 +985,16 @@ int sm_count(int device) {
   return cached[device];
 }
 
+// The shared prefix of a SHARED call: its page ids, how its work is split, and the
+// workspace of its segments.
+struct SharedPrefix {
+  const int32_t* table = nullptr;
+  PrefixWork work;
+  float* ws_o = nullptr;
+  float* ws_lse = nullptr;
+  float scale = 0.f;
+};
+
 // Launch geometry and workspace size of one decode call.
 struct DecodePlan {
   bool streamed = false;
@@ -923,9 +1045,16 @@ DecodePlan make_plan(int B, int Hq, int Hkv, int max_pages_per_seq, int nsm) {
   return pl;
 }
 
-template <int G>
+template <int G, bool SHARED>
 int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensorMap& tmK,
-                   const CUtensorMap& tmV, cudaStream_t stream, int device) {
+                   const CUtensorMap& tmV, const SharedPrefix* pre, cudaStream_t stream,
+                   int device) {
+  // The shared prefix comes right after the scan (streamed: overlapping it and the
+  // stream kernel) or first of all (direct).
+  auto prefix = [&](bool overlap) {
+    return launch_prefix(prm.q, prm.kc, prm.vc, prm.pw, pre->table, pre->ws_o, pre->ws_lse, prm.B,
+                         prm.Hq, prm.Hkv, prm.num_pages, pre->scale, overlap, stream, device);
+  };
   if (pl.streamed) {
     const int smem = pl.nstages * 2 * stage_kv_bytes(prm.Hkv) + 1024 +
                      (prm.hb_in_smem ? (prm.B + 1) * 4 : 0);
@@ -936,7 +1065,7 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
       std::lock_guard<std::mutex> g(mu);
       if (device < 0 || device >= 64) return set_error(FA_ERR_CUDA, "device ordinal out of range");
       if (attr_gen[device] != cache_generation()) {
-        cudaError_t e = cudaFuncSetAttribute(fa_decode_stream_kernel<G>,
+        cudaError_t e = cudaFuncSetAttribute(fa_decode_stream_kernel<G, SHARED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kStreamSmemBudget + 1024 + kHbSmemMax * 4);
         if (e != cudaSuccess)
@@ -954,19 +1083,31 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    fa_decode_scan_kernel<<<1, 1024, 0, stream>>>(prm);
+    fa_decode_scan_kernel<SHARED><<<1, 1024, 0, stream>>>(prm);
+    if constexpr (SHARED) {
+      const int rc = prefix(true);
+      if (rc != FA_OK) return rc;
+    }
     cfg.gridDim = dim3(pl.nctas);
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = smem;
-    cudaLaunchKernelEx(&cfg, fa_decode_stream_kernel<G>, tmK, tmV, prm);
+    cudaLaunchKernelEx(&cfg, fa_decode_stream_kernel<G, SHARED>, tmK, tmV, prm);
     cfg.gridDim = dim3(prm.B);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.dynamicSmemBytes = 0;
-    cudaLaunchKernelEx(&cfg, fa_decode_stream_merge_kernel, prm);
+    cudaLaunchKernelEx(&cfg, fa_decode_stream_merge_kernel<SHARED>, prm);
   } else {
+    if constexpr (SHARED) {
+      const int rc = prefix(false);
+      if (rc != FA_OK) return rc;
+    }
     dim3 grid(pl.nsplit, prm.B);
-    fa_decode_split_kernel<G><<<grid, kDecThreads, 0, stream>>>(prm);
-    fa_decode_combine_kernel<<<prm.B * prm.Hq, kDecD, 0, stream>>>(prm);
+    fa_decode_split_kernel<G, SHARED><<<grid, kDecThreads, 0, stream>>>(prm);
+    if constexpr (SHARED)
+      fa_decode_shared_combine_kernel<<<(prm.B * prm.Hq + kDecWarps - 1) / kDecWarps, kDecThreads,
+                                        0, stream>>>(prm);
+    else
+      fa_decode_combine_kernel<<<prm.B * prm.Hq, kDecD, 0, stream>>>(prm);
   }
   return FA_OK;
 }
@@ -975,7 +1116,7 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
 int run_decode(const void* q, const void* kcache, const void* vcache, const int32_t* block_table,
                const int32_t* seq_lens, void* o, float* lse, int B, int Hq, int Hkv,
                int max_pages_per_seq, int num_pages, float scale, const DecodePlan& pl, void* ws,
-               cudaStream_t stream, int device) {
+               cudaStream_t stream, int device, const SharedPrefix* pre = nullptr) {
   const int G = Hq / Hkv;
   DecodeParams prm;
   prm.q = static_cast<const uint16_t*>(q);
@@ -999,6 +1140,14 @@ int run_decode(const void* q, const void* kcache, const void* vcache, const int3
   prm.scale_log2 = scale * kLog2e;
   prm.err = device_error_word(device);
   if (!prm.err) return set_error(FA_ERR_CUDA, "device error word unavailable");
+  prm.pw = PrefixWork{};
+  prm.pre_o = prm.pre_lse = nullptr;
+  if (pre) {
+    prm.pw = pre->work;
+    prm.pw.err = prm.err;
+    prm.pre_o = pre->ws_o;
+    prm.pre_lse = pre->ws_lse;
+  }
   if (!pl.streamed && (pl.nsplit > 65535 || B > 65535))
     return set_error(FA_ERR_UNSUPPORTED, "too many sequences or chunks for one launch");
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL)
@@ -1024,12 +1173,16 @@ int run_decode(const void* q, const void* kcache, const void* vcache, const int3
     memset(&tmV, 0, sizeof(tmV));
   }
   int lrc;
+#define FA_DECODE_G(G_)                                                                  \
+  lrc = pre ? launch_kernels<G_, true>(prm, pl, tmK, tmV, pre, stream, device)             \
+            : launch_kernels<G_, false>(prm, pl, tmK, tmV, pre, stream, device)
   switch (G) {
-    case 1: lrc = launch_kernels<1>(prm, pl, tmK, tmV, stream, device); break;
-    case 2: lrc = launch_kernels<2>(prm, pl, tmK, tmV, stream, device); break;
-    case 4: lrc = launch_kernels<4>(prm, pl, tmK, tmV, stream, device); break;
-    default: lrc = launch_kernels<8>(prm, pl, tmK, tmV, stream, device); break;
+    case 1: FA_DECODE_G(1); break;
+    case 2: FA_DECODE_G(2); break;
+    case 4: FA_DECODE_G(4); break;
+    default: FA_DECODE_G(8); break;
   }
+#undef FA_DECODE_G
   if (lrc != FA_OK) return lrc;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(FA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
@@ -1059,6 +1212,57 @@ int launch_decode(const void* q, const void* kcache, const void* vcache, const i
                      cudaGetErrorString(e));
   rc = run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, max_pages_per_seq,
                   num_pages, scale, pl, ws, stream, device);
+  cudaError_t ef = cudaFreeAsync(ws, stream);
+  if (rc != FA_OK) return rc;
+  if (ef != cudaSuccess)
+    return set_error(FA_ERR_CUDA, "workspace release: %s", cudaGetErrorString(ef));
+  return FA_OK;
+}
+
+int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
+                         const int32_t* block_table, const int32_t* seq_lens,
+                         const int32_t* prefix_table, const int32_t* prefix_pages,
+                         int max_prefix_pages, void* o, float* lse, int B, int Hq, int Hkv,
+                         float scale, int max_pages_per_seq, int num_pages, cudaStream_t stream,
+                         int device) {
+  const int G = Hq / Hkv;
+  const int nsm = sm_count(device);
+  if (nsm <= 0) return set_error(FA_ERR_CUDA, "cannot read the SM count of device %d", device);
+  DecodePlan pl = make_plan(B, Hq, Hkv, max_pages_per_seq, nsm);
+  if (pl.streamed) {
+    // a CTA never gets more units than this, so no more slots are needed either
+    pl.dyn_units_cap = std::min(pl.dyn_units_cap, pl.nctas * kMaxUnitsPerCta);
+    finish_plan(pl, B, Hq, Hkv);
+  }
+  SharedPrefix pre;
+  pre.table = prefix_table;
+  pre.scale = scale;
+  pre.work.pages = prefix_pages;
+  pre.work.max_pages = max_prefix_pages;
+  const long long pairs = (static_cast<long long>(B) * G + 255) / 256;
+  const long long items = pairs * Hkv;
+  const long long tiles =
+      (static_cast<long long>(max_prefix_pages) * kPage + kPrefixTile - 1) / kPrefixTile;
+  if (items * tiles > 0x7fffffffLL - nsm || static_cast<long long>(B) * Hq > 0x7fffffffLL - 256)
+    return set_error(FA_ERR_UNSUPPORTED, "shared prefix: too much work for one call");
+  pre.work.pairs = static_cast<int>(pairs);
+  pre.work.items = static_cast<int>(items);
+  pre.work.ctas = nsm;
+  // segments write to slot CTA + item
+  const size_t pre_rows = static_cast<size_t>(nsm + items) * 256;
+  const size_t pre_bytes = (pre_rows * (kDecD + 1) * sizeof(float) + 255) & ~size_t(255);
+  cudaMemPool_t pool;
+  int rc = get_pool(device, &pool);
+  if (rc != FA_OK) return rc;
+  void* ws = nullptr;
+  cudaError_t e = cudaMallocFromPoolAsync(&ws, pre_bytes + pl.bytes, pool, stream);
+  if (e != cudaSuccess)
+    return set_error(FA_ERR_CUDA, "workspace allocation (%zu bytes): %s", pre_bytes + pl.bytes,
+                     cudaGetErrorString(e));
+  pre.ws_o = static_cast<float*>(ws);
+  pre.ws_lse = pre.ws_o + pre_rows * kDecD;
+  rc = run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, max_pages_per_seq,
+                  num_pages, scale, pl, static_cast<char*>(ws) + pre_bytes, stream, device, &pre);
   cudaError_t ef = cudaFreeAsync(ws, stream);
   if (rc != FA_OK) return rc;
   if (ef != cudaSuccess)

@@ -139,8 +139,29 @@ struct ExtendArgs {
 constexpr int kMaxExtendSeqs = 16384;   // three ints each in shared memory
 int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device);
 
+// Shared-prefix attention: how its work is split (see prefix_split.cuh).
+constexpr int kPrefixTile = 128;        // keys per tile
+constexpr int kPrefixMinTiles = 2;      // key tiles that a CTA takes at least
+struct PrefixWork {
+  const int32_t* pages = nullptr;       // number of shared pages, on the device
+  int max_pages = 0;                    // bound on it
+  int pairs = 0;                        // 256-row pairs of a KV head's B * G rows
+  int items = 0;                        // Hkv * pairs
+  int ctas = 0;                         // grid of the prefix kernel
+  int* err = nullptr;
+};
+int launch_prefix(const void* q, const void* kcache, const void* vcache, const PrefixWork& w,
+                  const int32_t* prefix_table, float* ws_o, float* ws_lse, int B, int Hq, int Hkv,
+                  int num_pages, float scale, bool overlap, cudaStream_t stream, int device);
+int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
+                         const int32_t* block_table, const int32_t* seq_lens,
+                         const int32_t* prefix_table, const int32_t* prefix_pages,
+                         int max_prefix_pages, void* o, float* lse, int B, int Hq, int Hkv,
+                         float scale, int max_pages_per_seq, int num_pages, cudaStream_t stream,
+                         int device);
+
 // Raises a kernel's dynamic shared-memory limit, once per device and context.
-enum SmemKernel : int { kSmemExtend = 0, kSmemKernels };
+enum SmemKernel : int { kSmemExtend = 0, kSmemPrefix, kSmemKernels };
 int raise_smem_limit(const void* kernel, int bytes, int device, SmemKernel which);
 
 // Release cached per-device resources owned by the decode path.

@@ -1,0 +1,54 @@
+// How the shared-prefix attention is split: used by the kernel that computes the
+// segments and by the merge that reads them.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "ptx_sm100.cuh"
+
+namespace fa {
+
+// floor(c * H / C) for 0 <= c <= C
+__device__ __forceinline__ int share_edge(int c, int H, int C) {
+  const long long prod = static_cast<long long>(c) * H;
+  if (prod <= 0x7fffffffLL)
+    return static_cast<int>(static_cast<uint32_t>(prod) / static_cast<uint32_t>(C));
+  return static_cast<int>(prod / C);
+}
+// The largest c in [0, C) with share_edge(c) <= x, for 0 <= x < H: the share that holds
+// entry x.
+__device__ __forceinline__ int cta_of(long long x, long long H, long long C) {
+  if ((x + 1) * C <= 0x7fffffffLL)             // the usual case: 32-bit division
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(C) - 1u) /
+                            static_cast<uint32_t>(H));
+  return static_cast<int>(((x + 1) * C - 1) / H);
+}
+
+// Number of shared pages, read on the device; a count outside [0, max_pages] is flagged
+// and stands for no sharing.
+__device__ __forceinline__ int shared_pages(const PrefixWork& w) {
+  const int n = __ldg(w.pages);
+  if (n < 0 || n > w.max_pages) {
+    atomicOr(w.err, kErrBadIndex);
+    return 0;
+  }
+  return n;
+}
+
+struct PrefixSplit {
+  int pages;       // shared pages
+  int nt;          // key tiles of the prefix
+  int units;       // items * nt
+  int ctas;        // CTAs that take a share (0: no prefix)
+};
+__device__ __forceinline__ PrefixSplit prefix_split(const PrefixWork& w, int C) {
+  PrefixSplit s;
+  s.pages = shared_pages(w);
+  s.nt = (s.pages * 16 + kPrefixTile - 1) / kPrefixTile;
+  s.units = w.items * s.nt;
+  s.ctas = min(C, (s.units + kPrefixMinTiles - 1) / kPrefixMinTiles);
+  return s;
+}
+
+}  // namespace fa

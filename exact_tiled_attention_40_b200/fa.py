@@ -50,6 +50,8 @@ _SIGS = {
     "fa_decode_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _I, _P]),
     "fa_decode_paged_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _I,
                                      _P]),
+    "fa_decode_shared_prefix": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P,
+                                     _I, _I, _I, _P]),
     "fa_extend_pages": (_I, [_P] * 10 + [_I] * 5 + [_P]),
     "fa_qk_norm_rope": (_I, _NORM_ROPE),
     "fa_qk_norm_rope_fp16": (_I, _NORM_ROPE),
@@ -429,6 +431,48 @@ def decode_paged_noalloc(q, kcache, vcache, block_table, seq_lens, o, lse=None, 
                                          _ptr(seq_lens), _ptr(o), B, Hq, Hkv, D, page_size,
                                          float(scale), s, block_table.shape[1], num_pages,
                                          _ptr(lse)), "fa_decode_paged_noalloc")
+
+
+def fa_decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages,
+                            o, B, Hq, Hkv, D, page_size, scale, max_pages_per_seq,
+                            max_prefix_pages, num_pages, lse=None, stream=None):
+    """Raw call of the C entry point."""
+    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    _check(lib().fa_decode_shared_prefix(
+        _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seq_lens),
+        _ptr(prefix_table), _ptr(prefix_pages), _ptr(o), B, Hq, Hkv, D, page_size, float(scale), s,
+        max_pages_per_seq, max_prefix_pages, num_pages, _ptr(lse)), "fa_decode_shared_prefix")
+
+
+def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages,
+                         scale=None, return_lse=True):
+    """decode_paged for a batch whose sequences share their first pages: the first
+    prefix_pages[0] (int32, on the device) entries of prefix_table [max_prefix_pages]
+    (a row of block_table will do).  Sequences shorter than the shared pages take no
+    part and are read through their own block_table row."""
+    where = "decode_shared_prefix"
+    _on_current_device(where, q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages)
+    _dtypes(where, torch.bfloat16, q=q, kcache=kcache, vcache=vcache)
+    _dtypes(where, torch.int32, block_table=block_table, seq_lens=seq_lens,
+            prefix_table=prefix_table, prefix_pages=prefix_pages)
+    _shape(where, "q", q, (None, None, None))
+    B, Hq, D = q.shape
+    _shape(where, "kcache", kcache, (None, None, None, D))
+    num_pages, page_size, Hkv, _ = kcache.shape
+    _shape(where, "vcache", vcache, tuple(kcache.shape))
+    _shape(where, "block_table", block_table, (B, None))
+    _shape(where, "seq_lens", seq_lens, (B,))
+    _shape(where, "prefix_table", prefix_table, (None,))
+    _shape(where, "prefix_pages", prefix_pages, (1,))
+    if scale is None:
+        scale = D ** -0.5
+    o = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    fa_decode_shared_prefix(q.contiguous(), kcache.contiguous(), vcache.contiguous(),
+                            block_table.contiguous(), seq_lens.contiguous(),
+                            prefix_table.contiguous(), prefix_pages, o, B, Hq, Hkv, D, page_size,
+                            scale, block_table.shape[1], prefix_table.shape[0], num_pages, lse)
+    return o, lse
 
 
 def fa_extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, seq_lens_out,

@@ -329,6 +329,34 @@ int fa_decode_paged_noalloc(const void* q, const void* kcache, const void* vcach
                             fa_stream_t stream, int max_pages_per_seq, int num_pages, float* lse);
 
 /*
+ * Paged decode of a batch whose sequences share their first pages (a common
+ * system prompt, many samples of one document): attention over the shared keys
+ * is computed for the whole batch at once, so they are read once instead of once
+ * per sequence, and joined with each sequence's own keys by the LSE.
+ *
+ * The result is fa_decode_paged's on the same q, caches, block_table and
+ * seq_lens (within rounding), with its layouts, supported sizes and rules, if
+ *   prefix_table  [max_prefix_pages] int32 page ids in token order
+ *   prefix_pages  [1] int32 on the device: the first prefix_pages[0] entries of
+ *                 prefix_table are the first pages of every sequence of at least
+ *                 16 * prefix_pages[0] tokens.  Those entries of such a sequence's
+ *                 block_table row are not read; a row of block_table may itself be
+ *                 passed as prefix_table.
+ * Shorter sequences (the empty rows of a padded batch among them) take no part in
+ * the sharing: all their keys are read through their own block_table row.
+ * 0 <= max_prefix_pages <= max_pages_per_seq; with 0 both pointers may be NULL.
+ * A prefix_pages[0] outside [0, max_prefix_pages] raises FA_ERR_DEVICE_INDEX and
+ * counts as 0; so does an id of the shared pages outside [0, num_pages), whose 16
+ * keys then count as zero vectors.  The workspace is taken as by fa_decode_paged.
+ */
+int fa_decode_shared_prefix(const void* q, const void* kcache, const void* vcache,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* prefix_table, const int32_t* prefix_pages, void* o,
+                            int B, int Hq, int Hkv, int D, int page_size, float scale,
+                            fa_stream_t stream, int max_pages_per_seq, int max_prefix_pages,
+                            int num_pages, float* lse);
+
+/*
  * Block tables, positions and cache slots of one step's new tokens, from request
  * lengths and a list of free pages, all on the device.
  *   seq_lens, new_lens  [B] int32: tokens in the cache and tokens to add (0 or more)

@@ -142,6 +142,30 @@ def test_extend_rejects(lib, kw, code):
     assert extend(lib, **kw) == code
 
 
+def shared(lib, q=at(1), kc=at(2), vc=at(3), table=at(4), lens=at(5), prefix=at(6), pages=at(7),
+           o=at(8), B=2, Hq=8, Hkv=2, D=128, page=16, scale=0.1, maxp=9, max_prefix=4, npages=20):
+    return lib.fa_decode_shared_prefix(q, kc, vc, table, lens, prefix, pages, o, B, Hq, Hkv, D,
+                                       page, scale, None, maxp, max_prefix, npages, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(D=64), UNSUPPORTED), (dict(page=32), UNSUPPORTED), (dict(Hq=6), UNSUPPORTED),
+    (dict(Hq=5), INVALID), (dict(B=-1), INVALID), (dict(maxp=0), INVALID), (dict(npages=0), INVALID),
+    (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(kc=at(2) + 8), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(max_prefix=-1), INVALID), (dict(max_prefix=10), INVALID), (dict(prefix=None), INVALID),
+    (dict(pages=None), INVALID), (dict(prefix=at(6) + 2), INVALID)])
+def test_shared_prefix_rejects(lib, kw, code):
+    assert shared(lib, **kw) == code
+
+
+@NO_DEVICE_ONLY
+def test_shared_prefix_accepts(lib):
+    assert shared(lib) == E["FA_ERR_NO_DEVICE"]
+    assert shared(lib, max_prefix=0, prefix=None, pages=None) == E["FA_ERR_NO_DEVICE"]
+    assert shared(lib, B=0) == 0
+
+
 def test_the_binding_refuses_host_tensors():
     i = torch.zeros(2, 3, dtype=torch.int32)
     x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
@@ -151,6 +175,7 @@ def test_the_binding_refuses_host_tensors():
         lambda: fa.qk_norm_rope(x, x, w, w, tab, i[:1, :2]),
         lambda: fa.qk_norm_rope_backward(x, x, x, x, w, w, tab, i[:1, :2]),
         lambda: fa.append_paged(x[0], x[0], x[0], x, x, i[0].long(), w, w, tab, i[:1, :2]),
+        lambda: fa.decode_shared_prefix(x[0], x, x, i, i[0], i[0], i[0, :1]),
     ]
     for call in calls:
         with pytest.raises(fa.FAError, match="CUDA device"):
