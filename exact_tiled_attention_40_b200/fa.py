@@ -100,36 +100,56 @@ def _check(code: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The handle alone costs a tenth of the microsecond or two that a Stream object takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if _raw_stream is None or index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(index)
 
 
+# Checks of the calls that a serving step makes once a layer: a few hundred nanoseconds
+# each counts there, so the texts are put together only for a refusal.
 def _on_current_device(where, *tensors):
     """The kernels run on the current device: refuses tensors (None: absent) elsewhere."""
+    current = None
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+        if t is None:
+            continue
+        if current is None and t.is_cuda:
+            current = torch.cuda.current_device()
+        if not t.is_cuda or t.get_device() != current:
             raise FAError(1, where, "tensors must live on the current CUDA device")
 
 
-def _dtypes(where, dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise FAError(1, where, f"{name} must be {str(dtype)[6:]}, not {str(t.dtype)[6:]}")
+def _dtypes(where, dtype, *tensors):
+    for t in tensors:
+        if t is not None and t.dtype is not dtype:
+            raise FAError(1, where, f"a tensor of shape {list(t.shape)} must be {str(dtype)[6:]}, "
+                          f"not {str(t.dtype)[6:]}")
 
 
-def _shape(where, name, t, want):
-    """Refuses t unless its shape is `want` (None: any size)."""
-    if t.dim() != len(want) or any(w is not None and w != n for w, n in zip(want, t.shape)):
+def _shape(where, name, t, *want):
+    if t.shape != want:
         raise FAError(1, where, f"{name} must have shape {list(want)}, not {list(t.shape)}")
+
+
+def _dims(where, name, t, n):
+    if t.dim() != n:
+        raise FAError(1, where, f"{name} must have {n} dimensions, not {t.dim()}")
+    return t.shape
 
 
 def _aligned16(t):
     """t (or None) contiguous and at a 16-byte boundary, copied where it is not."""
-    if t is None:
-        return None
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
     t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
@@ -137,7 +157,7 @@ def _aligned16(t):
 def fa_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, causal, stream=None):
     """Raw call of the C entry point (bf16 or fp16 chosen from q's dtype)."""
     fn = lib().fa_fwd if q.dtype == torch.bfloat16 else lib().fa_fwd_fp16
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, D,
               float(scale), int(bool(causal)), s), "fa_fwd")
 
@@ -164,7 +184,7 @@ def fa_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, B, Hq, Hkv, max_q, max_k, total_q
                   scale, causal, stream=None):
     """Raw call of the ragged-batch entry point (bf16 or fp16 chosen from q's dtype)."""
     fn = lib().fa_fwd_varlen if q.dtype == torch.bfloat16 else lib().fa_fwd_varlen_fp16
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(cu_k), B, Hq, Hkv,
               max_q, max_k, total_q, total_k, D, float(scale), int(bool(causal)), s),
            "fa_fwd_varlen")
@@ -198,7 +218,7 @@ def attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
 def fa_fwd_paged(q, kcache, vcache, block_table, o, lse, cu_q, seq_lens_k, B, Hq, Hkv, max_q,
                  max_pages_per_seq, num_pages, total_q, D, page_size, scale, causal, stream=None):
     """Raw call of the paged-prefill entry point (bf16)."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_fwd_paged(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(o),
                               _ptr(lse), _ptr(cu_q), _ptr(seq_lens_k), B, Hq, Hkv, max_q,
                               max_pages_per_seq, num_pages, total_q, D, page_size, float(scale),
@@ -230,7 +250,7 @@ def fa_fwd_host(q_host, k_host, v_host, o_host, lse_host, q, k, v, o, lse, B, Hq
                 D, scale, causal, stream=None):
     """Raw call of the host-buffer forward (bf16): *_host are CPU tensors, the others
     the device staging tensors of the same shapes."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_fwd_host(_ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(o_host),
                              _ptr(lse_host), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq,
                              Hkv, Nq, Nk, D, float(scale), int(bool(causal)), s), "fa_fwd_host")
@@ -267,7 +287,7 @@ def attention_from_host(q_host, k_host, v_host, scale=None, causal=False, device
 
 def fa_quantize_e4m3(x, codes, scales, Z, N, D, group_rows, signs=None, stream=None):
     """Raw call of the E4M3 quantiser's C entry point."""
-    s = _stream(x.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(x.device) if stream is None else stream
     _check(lib().fa_quantize_e4m3(_ptr(x), _ptr(codes), _ptr(scales), Z, N, D, group_rows,
                                   _ptr(signs), s), "fa_quantize_e4m3")
 
@@ -296,7 +316,7 @@ def quantize_e4m3(x: torch.Tensor, group_rows: int = 128, signs: torch.Tensor | 
 def fa_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, o, lse, B, Hq, Hkv, Nq, Nk, D, scale,
                causal, stream=None):
     """Raw call of the FP8 forward's C entry point."""
-    s = _stream(q8.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q8.device) if stream is None else stream
     _check(lib().fa_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(v8), _ptr(q_scale), _ptr(k_scale),
                             _ptr(v_scale), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, D, float(scale),
                             int(bool(causal)), s), "fa_fwd_fp8")
@@ -343,7 +363,7 @@ def attention_fp8(q, k, v, scale=None, causal=False, signs=None, return_lse=True
 def fa_bwd(q, k, v, o, lse, dout, dq, dk, dv, delta, B, Hq, Hkv, Nq, Nk, D, scale, causal,
            stream=None):
     """Raw call of the backward's C entry point."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq),
                         _ptr(dk), _ptr(dv), _ptr(delta), B, Hq, Hkv, Nq, Nk, D, float(scale),
                         int(bool(causal)), s), "fa_bwd")
@@ -386,7 +406,7 @@ def merge_partials(o_acc, lse_acc, o_part, lse_part, first=False, o_out=None, st
         raise FAError(1, "merge_partials", "o_out must be a contiguous bf16 tensor like o_part")
     D = o_part.shape[-1]
     rows = lse_part.numel()
-    s = _stream(o_part.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(o_part.device) if stream is None else stream
     _check(lib().fa_merge_partials(_ptr(o_acc), _ptr(lse_acc), _ptr(o_part), _ptr(lse_part),
                                    _ptr(o_out), rows, D, int(bool(first)), s),
            "fa_merge_partials")
@@ -395,7 +415,7 @@ def merge_partials(o_acc, lse_acc, o_part, lse_part, first=False, o_out=None, st
 def fa_decode_paged(q, kcache, vcache, block_table, seq_lens, o, B, Hq, Hkv, D, page_size, scale,
                     max_pages_per_seq, num_pages, lse=None, stream=None):
     """Raw call of the C entry point."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_decode_paged(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table),
                                  _ptr(seq_lens), _ptr(o), B, Hq, Hkv, D, page_size, float(scale),
                                  s, max_pages_per_seq, num_pages, _ptr(lse)), "fa_decode_paged")
@@ -426,7 +446,7 @@ def decode_paged_noalloc(q, kcache, vcache, block_table, seq_lens, o, lse=None, 
     num_pages, page_size, Hkv, _ = kcache.shape
     if scale is None:
         scale = D ** -0.5
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_decode_paged_noalloc(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table),
                                          _ptr(seq_lens), _ptr(o), B, Hq, Hkv, D, page_size,
                                          float(scale), s, block_table.shape[1], num_pages,
@@ -437,7 +457,7 @@ def fa_decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_tab
                             o, B, Hq, Hkv, D, page_size, scale, max_pages_per_seq,
                             max_prefix_pages, num_pages, lse=None, stream=None):
     """Raw call of the C entry point."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_decode_shared_prefix(
         _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(seq_lens),
         _ptr(prefix_table), _ptr(prefix_pages), _ptr(o), B, Hq, Hkv, D, page_size, float(scale), s,
@@ -452,18 +472,17 @@ def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
     part and are read through their own block_table row."""
     where = "decode_shared_prefix"
     _on_current_device(where, q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages)
-    _dtypes(where, torch.bfloat16, q=q, kcache=kcache, vcache=vcache)
-    _dtypes(where, torch.int32, block_table=block_table, seq_lens=seq_lens,
-            prefix_table=prefix_table, prefix_pages=prefix_pages)
-    _shape(where, "q", q, (None, None, None))
-    B, Hq, D = q.shape
-    _shape(where, "kcache", kcache, (None, None, None, D))
-    num_pages, page_size, Hkv, _ = kcache.shape
-    _shape(where, "vcache", vcache, tuple(kcache.shape))
-    _shape(where, "block_table", block_table, (B, None))
-    _shape(where, "seq_lens", seq_lens, (B,))
-    _shape(where, "prefix_table", prefix_table, (None,))
-    _shape(where, "prefix_pages", prefix_pages, (1,))
+    _dtypes(where, torch.bfloat16, q, kcache, vcache)
+    _dtypes(where, torch.int32, block_table, seq_lens, prefix_table, prefix_pages)
+    B, Hq, D = _dims(where, "q", q, 3)
+    num_pages, page_size, Hkv, _ = cache = _dims(where, "kcache", kcache, 4)
+    _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
+    _shape(where, "vcache", vcache, *cache)
+    _, max_pages = _dims(where, "block_table", block_table, 2)
+    _shape(where, "block_table", block_table, B, max_pages)
+    _shape(where, "seq_lens", seq_lens, B)
+    max_prefix, = _dims(where, "prefix_table", prefix_table, 1)
+    _shape(where, "prefix_pages", prefix_pages, 1)
     if scale is None:
         scale = D ** -0.5
     o = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
@@ -471,7 +490,7 @@ def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
     fa_decode_shared_prefix(q.contiguous(), kcache.contiguous(), vcache.contiguous(),
                             block_table.contiguous(), seq_lens.contiguous(),
                             prefix_table.contiguous(), prefix_pages, o, B, Hq, Hkv, D, page_size,
-                            scale, block_table.shape[1], prefix_table.shape[0], num_pages, lse)
+                            scale, max_pages, max_prefix, num_pages, lse)
     return o, lse
 
 
@@ -479,7 +498,7 @@ def fa_extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, seq
                     free_count_out, cu_seqlens_q, positions, slot_map, B, max_pages_per_seq,
                     num_pages, page_size, max_tokens, stream=None):
     """Raw call of the C entry point."""
-    s = _stream(block_table.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(block_table.device) if stream is None else stream
     _check(lib().fa_extend_pages(
         _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), _ptr(free_pages), _ptr(free_count),
         _ptr(seq_lens_out), _ptr(free_count_out), _ptr(cu_seqlens_q), _ptr(positions),
@@ -495,24 +514,20 @@ def extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, num_pa
     int64, pages left [1])."""
     where = "extend_pages"
     _on_current_device(where, block_table, seq_lens, new_lens, free_pages, free_count)
-    _dtypes(where, torch.int32, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens,
-            free_pages=free_pages, free_count=free_count)
-    _shape(where, "block_table", block_table, (None, None))
-    B, max_pages = block_table.shape
-    _shape(where, "seq_lens", seq_lens, (B,))
-    _shape(where, "new_lens", new_lens, (B,))
-    _shape(where, "free_pages", free_pages, (num_pages,))
-    _shape(where, "free_count", free_count, (1,))
+    _dtypes(where, torch.int32, block_table, seq_lens, new_lens, free_pages, free_count)
+    B, max_pages = _dims(where, "block_table", block_table, 2)
+    _shape(where, "seq_lens", seq_lens, B)
+    _shape(where, "new_lens", new_lens, B)
+    _shape(where, "free_pages", free_pages, num_pages)
+    _shape(where, "free_count", free_count, 1)
     if not block_table.is_contiguous():
         raise FAError(1, where, "block_table is written in place and must be contiguous")
-    dev = block_table.device
     if max_tokens < 0:
         raise FAError(1, where, "max_tokens must not be negative")
-    lens_out = torch.empty(B, dtype=torch.int32, device=dev)
-    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    dev = block_table.device
+    lens_out, cu, left, positions = torch.empty(
+        2 * B + 2 + max_tokens, dtype=torch.int32, device=dev).split((B, B + 1, 1, max_tokens))
     slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-    left = torch.empty(1, dtype=torch.int32, device=dev)
     fa_extend_pages(block_table, seq_lens.contiguous(), new_lens.contiguous(),
                     free_pages.contiguous(), free_count, lens_out, left, cu, positions, slots, B,
                     max_pages, num_pages, 16, max_tokens)
@@ -523,52 +538,51 @@ def _head_rows(t):
     """t [..., H, D] as the library reads token-major rows: t itself where each token's
     heads are contiguous and one stride leads from token to token (a view of a QKV
     projection), a contiguous copy otherwise; and that stride in elements."""
-    lead, (H, D), st = t.shape[:-2], t.shape[-2:], t.stride()
-    stride = H * D                              # no step from token to token: any will do
-    for n, s in zip(reversed(lead), reversed(st[:-2])):
-        if n > 1:
-            stride = s
-            break
-    span = 1
-    for n, s in zip(reversed(lead), reversed(st[:-2])):
-        if n > 1 and s != stride * span:
-            return _aligned16(t), H * D
-        span *= n
-    if (st[-1] == 1 and (H == 1 or st[-2] == D) and stride >= H * D and stride % 8 == 0
-            and t.data_ptr() % 16 == 0):
+    *lead, H, D = t.shape
+    *steps, across, inner = t.stride()
+    stride, span = H * D, 1                     # no step from token to token: any will do
+    for i in range(len(lead) - 1, -1, -1):
+        if lead[i] != 1:
+            if span == 1:
+                stride = steps[i]
+            elif steps[i] != stride * span:
+                return _aligned16(t.contiguous()), H * D
+            span *= lead[i]
+    if (inner == 1 and (across == D or H == 1) and stride >= H * D and stride % 8 == 0
+            and span and t.data_ptr() % 16 == 0):
         return t, stride
-    return _aligned16(t), H * D
+    return _aligned16(t.contiguous()), H * D
 
 
 def _norm_rope_args(where, q, k, q_weight, k_weight, table, positions, pair_axis, lead):
-    """Checks shared by the norm + rotation calls; the leading sizes, heads and sizes of
-    the table, and contiguous weights, table, positions and axes."""
-    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis)
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    """Checks shared by the norm + rotation calls; contiguous weights, table, positions and
+    axes, and the sizes of the table."""
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise FAError(1, where, "q must be bf16 or fp16")
-    _dtypes(where, q.dtype, k=k, q_weight=q_weight, k_weight=k_weight)
-    _dtypes(where, torch.float32, table=table)
-    _dtypes(where, torch.int32, positions=positions)
-    _dtypes(where, torch.uint8, pair_axis=pair_axis)
-    _shape(where, "q", q, (None,) * (lead + 2))
-    D = q.shape[-1]
-    _shape(where, "k", k, tuple(q.shape[:lead]) + (None, D))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _shape(where, name, w, (D,))
-    _shape(where, "table", table, (None, None))
-    max_pos, rot = table.shape
-    tokens = 1
-    for n in q.shape[:lead]:
-        tokens *= n
+    _dtypes(where, dtype, k, q_weight, k_weight)
+    _dtypes(where, torch.float32, table)
+    _dtypes(where, torch.int32, positions)
+    sizes = _dims(where, "q", q, lead + 2)
+    D = sizes[-1]
+    _shape(where, "k", k, *sizes[:lead], _dims(where, "k", k, lead + 2)[lead], D)
+    if q_weight is not None:
+        _shape(where, "q_weight", q_weight, D)
+    if k_weight is not None:
+        _shape(where, "k_weight", k_weight, D)
+    max_pos, rot = _dims(where, "table", table, 2)
+    tokens = sizes[0] if lead == 1 else sizes[0] * sizes[1]
     if positions.dim() == 1:
-        positions = positions[None]
-    _shape(where, "positions", positions, (None, tokens))
-    axes = positions.shape[0]
+        _shape(where, "positions", positions, tokens)
+        axes = 1
+    else:
+        axes = _dims(where, "positions", positions, 2)[0]
+        _shape(where, "positions", positions, axes, tokens)
     if axes != 1:
         if pair_axis is None:
             raise FAError(1, where, "pair_axis is needed with more than one axis")
-        _shape(where, "pair_axis", pair_axis, (rot // 2,))
+        _dtypes(where, torch.uint8, pair_axis)
+        _shape(where, "pair_axis", pair_axis, rot // 2)
         pair_axis = pair_axis.contiguous()
     return (_aligned16(q_weight), _aligned16(k_weight), _aligned16(table), positions.contiguous(),
             pair_axis, rot, max_pos, axes)
@@ -579,7 +593,7 @@ def fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out
                     heads_first, eps, stream=None):
     """Raw call of the C entry point (bf16 or fp16 chosen from q's dtype)."""
     fn = lib().fa_qk_norm_rope if q.dtype == torch.bfloat16 else lib().fa_qk_norm_rope_fp16
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(fn(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(table), _ptr(positions),
               _ptr(pair_axis), _ptr(q_out), _ptr(k_out), B, N, Hq, Hkv, D, q_stride, k_stride,
               rot_dim, max_positions, n_axes, int(bool(interleaved)), int(bool(heads_first)),
@@ -594,15 +608,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis=None, eps
     [n_axes, B * N] (or [B * N]) int32, pair j along axis pair_axis[j] (uint8).
     Returns q and k as [B, H, N, D] (heads_first, what `attention` takes) or [B, N, H, D]."""
     where = "qk_norm_rope"
+    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis)
     q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
         where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
     B, N, Hq, D = q.shape
     Hkv = k.shape[2]
     q, q_stride = _head_rows(q)
     k, k_stride = _head_rows(k)
-    shape = (lambda H: (B, H, N, D)) if heads_first else (lambda H: (B, N, H, D))
-    q_out = torch.empty(shape(Hq), dtype=q.dtype, device=q.device)
-    k_out = torch.empty(shape(Hkv), dtype=q.dtype, device=q.device)
+    dtype, dev = q.dtype, q.device
+    q_out = torch.empty((B, Hq, N, D) if heads_first else (B, N, Hq, D), dtype=dtype, device=dev)
+    k_out = torch.empty((B, Hkv, N, D) if heads_first else (B, N, Hkv, D), dtype=dtype, device=dev)
     fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N, Hq,
                     Hkv, D, q_stride, k_stride, rot, max_pos, axes, interleaved, heads_first, eps)
     return q_out, k_out
@@ -614,7 +629,7 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, table, positio
                         heads_first, eps, stream=None):
     """Raw call of the C entry point (bf16 or fp16 chosen from q's dtype)."""
     fn = lib().fa_qk_norm_rope_bwd if q.dtype == torch.bfloat16 else lib().fa_qk_norm_rope_bwd_fp16
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(fn(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight),
               _ptr(table), _ptr(positions), _ptr(pair_axis), _ptr(dq), _ptr(dk), _ptr(dq_weight),
               _ptr(dk_weight), _ptr(scratch), B, N, Hq, Hkv, D, q_stride, k_stride, dq_stride,
@@ -628,14 +643,18 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table, posit
     outputs: dq [B, N, Hq, D] and dk [B, N, Hkv, D] in q's dtype, the weights' in fp32
     (None where the weight is None)."""
     where = "qk_norm_rope_backward"
+    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis, dq_out, dk_out)
     q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
         where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
-    _on_current_device(where, dq_out, dk_out)
-    _dtypes(where, q.dtype, dq_out=dq_out, dk_out=dk_out)
+    _dtypes(where, q.dtype, dq_out, dk_out)
     B, N, Hq, D = q.shape
     Hkv = k.shape[2]
-    _shape(where, "dq_out", dq_out, (B, Hq, N, D) if heads_first else (B, N, Hq, D))
-    _shape(where, "dk_out", dk_out, (B, Hkv, N, D) if heads_first else (B, N, Hkv, D))
+    if heads_first:
+        _shape(where, "dq_out", dq_out, B, Hq, N, D)
+        _shape(where, "dk_out", dk_out, B, Hkv, N, D)
+    else:
+        _shape(where, "dq_out", dq_out, B, N, Hq, D)
+        _shape(where, "dk_out", dk_out, B, N, Hkv, D)
     q, q_stride = _head_rows(q)
     k, k_stride = _head_rows(k)
     dev = q.device
@@ -659,7 +678,7 @@ def fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis, sl
                     kcache, vcache, T, Hq, Hkv, D, page_size, num_pages, q_stride, k_stride,
                     v_stride, rot_dim, max_positions, n_axes, interleaved, eps, stream=None):
     """Raw call of the C entry point (bf16)."""
-    s = _stream(q.device) if stream is None else ctypes.c_void_p(stream)
+    s = _stream(q.device) if stream is None else stream
     _check(lib().fa_append_paged(
         _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(table), _ptr(positions),
         _ptr(pair_axis), _ptr(slot_map), _ptr(q_out), _ptr(kcache), _ptr(vcache), T, Hq, Hkv, D,
@@ -675,17 +694,19 @@ def append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table, p
     in place.  Returns q [T, Hq, D] for prefill_paged and the decode calls; rows of padding
     tokens are left unset."""
     where = "append_paged"
+    _on_current_device(where, q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table,
+                       positions, pair_axis)
+    _dtypes(where, torch.bfloat16, q, v, kcache, vcache)
+    _dtypes(where, torch.int64, slot_map)
     q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
         where, q, k, q_weight, k_weight, table, positions, pair_axis, 1)
-    _on_current_device(where, v, kcache, vcache, slot_map)
-    _dtypes(where, torch.bfloat16, q=q, v=v, kcache=kcache, vcache=vcache)
-    _dtypes(where, torch.int64, slot_map=slot_map)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    _shape(where, "v", v, (T, Hkv, D))
-    _shape(where, "kcache", kcache, (None, None, Hkv, D))
-    _shape(where, "vcache", vcache, tuple(kcache.shape))
-    _shape(where, "slot_map", slot_map, (T,))
+    _shape(where, "v", v, T, Hkv, D)
+    num_pages, page_size, _, _ = cache = _dims(where, "kcache", kcache, 4)
+    _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
+    _shape(where, "vcache", vcache, *cache)
+    _shape(where, "slot_map", slot_map, T)
     if not (kcache.is_contiguous() and vcache.is_contiguous()):
         raise FAError(1, where, "the caches are written in place and must be contiguous")
     q, q_stride = _head_rows(q)
@@ -693,8 +714,8 @@ def append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table, p
     v, v_stride = _head_rows(v)
     q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
     fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis,
-                    slot_map.contiguous(), q_out, kcache, vcache, T, Hq, Hkv, D, kcache.shape[1],
-                    kcache.shape[0], q_stride, k_stride, v_stride, rot, max_pos, axes, interleaved,
+                    slot_map.contiguous(), q_out, kcache, vcache, T, Hq, Hkv, D, page_size,
+                    num_pages, q_stride, k_stride, v_stride, rot, max_pos, axes, interleaved,
                     eps)
     return q_out
 

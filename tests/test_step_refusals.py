@@ -184,12 +184,14 @@ def test_the_binding_refuses_host_tensors():
 
 def test_the_binding_checks_shapes_and_types():
     with pytest.raises(fa.FAError, match="int32"):
-        fa._dtypes("f", torch.int32, lens=torch.zeros(3))
+        fa._dtypes("f", torch.int32, torch.zeros(3))
     with pytest.raises(fa.FAError, match="shape"):
-        fa._shape("f", "lens", torch.zeros(3), (4,))
+        fa._shape("f", "lens", torch.zeros(3), 4)
     with pytest.raises(fa.FAError, match="shape"):
-        fa._shape("f", "lens", torch.zeros(3, 1), (3,))
-    fa._shape("f", "lens", torch.zeros(3, 2), (None, 2))
+        fa._shape("f", "lens", torch.zeros(3, 1), 3)
+    with pytest.raises(fa.FAError, match="dimensions"):
+        fa._dims("f", "lens", torch.zeros(3, 1), 1)
+    fa._shape("f", "lens", torch.zeros(3, 2), 3, 2)
 
 
 def test_head_rows_reads_views_in_place_and_copies_the_rest():
