@@ -35,7 +35,12 @@
 // SHARED instantiations serve batches whose sequences share their first pages: the
 // shared keys are the business of fa_prefix_sm100.cu, the kernels here stream each
 // sequence's own keys behind them, and the merge joins both.  A sequence shorter than
-// the shared pages does not take part: all of its keys are streamed as its own.
+// the shared pages does not take part: all of its keys are streamed as its own.  They
+// always stream: where there are more KV heads than the 8 consumer warps, a sequence is
+// cut into groups of heads that go through all kernels as sequences of their own (q, o
+// and the LSE of a group are contiguous, and a stage's box starts at the group's first
+// head).  33 sequences of about 150 own keys, 16 heads, 4000 shared keys: 51.0 us direct,
+// 33.2 us cut in two.
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
@@ -59,6 +64,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // streamed schedule
 constexpr int kHalf = 8;                        // token slots per stage
+// SHARED: a stage is a page.  The consumers' chain of a stage (scores, maximum, exponents,
+// weights) is what bounds a CTA, and twice the tokens lengthen it little: a page of 8 KV
+// heads takes an SM 0.92 us, two half-pages 1.36 us; of 4 heads or fewer 0.68 and 1.16 us.
+constexpr int stage_tokens(bool shared) { return shared ? kPage : kHalf; }
 constexpr int kConsumerWarps = kDecWarps;       // one per KV head (see the stream kernel)
 constexpr int kStreamThreads = 12 * 32;          // 8 consumer warps + a producer warpgroup
 // Register split (setmaxnreg): the producer warpgroup (warps 8-11, one of them
@@ -77,10 +86,15 @@ constexpr int kStreamSmemBudget = 200 * 1024;
 // them over all sequences, so no sequence collects many partials.
 constexpr int kDynDiv = 16;    // 1 / kDynDiv of each share is dynamic
 constexpr int kDynUnit = 8;    // half-pages per dynamic unit (at least)
+// SHARED: the CTAs that the shared-prefix kernel keeps waiting only take dynamic units, and
+// how long they wait is estimated, so more is dynamic (64 sequences of about 2050 own and
+// 4096 shared keys: 104.5 us, 106.9 with units of 2 pages).
+constexpr int dyn_div(bool shared) { return shared ? 8 : kDynDiv; }
+constexpr int dyn_unit(bool shared) { return shared ? 4 : kDynUnit; }
 constexpr int kMaxUnitsPerCta = 4;
 constexpr int kMaxStreamCtas = 204;                       // so a sequence has <= 1024 partials
 constexpr int kMaxMergeSlots = kMaxStreamCtas * (1 + kMaxUnitsPerCta);
-constexpr int kMergeWarps = 32;
+constexpr int merge_warps(bool shared) { return shared ? 8 : 32; }
 constexpr int kHbSmemMax = 4096;   // sequences whose offsets the producer keeps in shared memory
 
 struct DecodeParams {
@@ -102,9 +116,12 @@ struct DecodeParams {
   int hb_in_smem;              // streamed: the producer copies hb to shared memory
   float scale_log2;
   int* err;
+  int merge_split;             // SHARED: warps of the merge that share a row (1, 2, 4 or 8)
+  int groups;                  // SHARED: head groups of a sequence (B, Hq, Hkv count these)
   PrefixWork pw;               // SHARED: the shared pages and how their work is split
   const float* pre_o;          // SHARED: segments' partial outputs [slot][256][128]
   const float* pre_lse;        // SHARED: their LSE [slot][256]
+  const int32_t* prefix_table; // SHARED: ids of the shared pages
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -128,6 +145,12 @@ __device__ __forceinline__ int checked_len(const DecodeParams& p, int b) {
   const int len = p.seq_lens[b];
   if (len < 0 || len > p.max_pages * kPage) return -1;
   return len;
+}
+
+// The sequence that entry b of the batch belongs to.
+template <bool SHARED>
+__device__ __forceinline__ int seq_of(const DecodeParams& p, int b) {
+  return SHARED ? b / p.groups : b;
 }
 
 // The keys that sequence b does not share: their number (-1: invalid length) and the
@@ -170,7 +193,7 @@ __device__ __forceinline__ float fold_heads(float (&v)[G], int sub) {
   return x;
 }
 
-template <int G, bool SHARED>
+template <int G>
 __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const DecodeParams p) {
   constexpr int LG = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   constexpr int SHIFT = 4 - LG;       // lane `h << SHIFT` holds head h after the fold
@@ -185,13 +208,11 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
   const int sub = lane & 15;
   const int my_head = sub >> SHIFT;
 
-  const int seq_len = checked_len(p, b);
-  if (seq_len < 0) {
+  const int len = checked_len(p, b);
+  if (len < 0) {
     if (threadIdx.x == 0 && split == 0) atomicOr(p.err, kErrBadIndex);
     return;
   }
-  const OwnKeys mine = own_keys<SHARED>(seq_len, SHARED ? shared_pages(p.pw) : 0);
-  const int len = mine.len;
   const int npages = (len + kPage - 1) / kPage;
   const int pbeg = split * p.pps;
   if (pbeg >= npages) return;
@@ -220,7 +241,7 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
     float m_mine = -INFINITY;
 
     for (int pg = pbeg; pg < pend; ++pg) {
-      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + mine.page0 + pg];
+      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + pg];
       if (page < 0 || page >= p.num_pages) {
         if (lane == 0) atomicOr(p.err, kErrBadIndex);
         continue;
@@ -329,8 +350,11 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
 // [Hkv heads][8 tokens][64 elements] with 128-byte swizzle: the 128-byte row of
 // (head g, token t) keeps its 16-byte chunk c at position c ^ t, so the 8 token
 // rows of one head are read by ldmatrix without bank conflicts.
-__host__ __device__ constexpr int box_bytes(int Hkv) { return Hkv * kHalf * 64 * 2; }
-__host__ __device__ constexpr int stage_kv_bytes(int Hkv) { return 2 * box_bytes(Hkv); }
+// (SHARED: of 16 tokens, whose swizzle is that of token % 8.)
+__host__ __device__ constexpr int box_bytes(int Hkv, int tokens) { return Hkv * tokens * 64 * 2; }
+__host__ __device__ constexpr int stage_kv_bytes(int Hkv, int tokens) {
+  return 2 * box_bytes(Hkv, tokens);
+}
 
 // hb[b] = sum over b' < b of ceil(len_b' / 8); hb[B] = total.  One block.
 // (SHARED: of the lengths without the shared keys.)
@@ -338,7 +362,8 @@ template <bool SHARED>
 __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams p) {
   __shared__ int warp_sums[32];
   __shared__ int carry;
-  const int shared = SHARED ? shared_pages(p.pw) : 0;
+  constexpr int TS = stage_tokens(SHARED);
+  const int shared = SHARED && p.pw.together ? shared_pages(p.pw) : 0;
   pdl_launch_dependents();   // the stream kernel may launch now; it waits for hb itself
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -350,11 +375,11 @@ __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams
     const int b = base + threadIdx.x;
     int v = 0;
     if (b < p.B) {
-      const int len = checked_len(p, b);
+      const int len = checked_len(p, seq_of<SHARED>(p, b));
       if (len < 0)
         atomicOr(p.err, kErrBadIndex);
       else
-        v = (own_keys<SHARED>(len, shared).len + kHalf - 1) / kHalf;
+        v = (own_keys<SHARED>(len, shared).len + TS - 1) / TS;
     }
     int x = v;   // inclusive warp scan
 #pragma unroll
@@ -393,13 +418,15 @@ __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams
 struct StreamSplit {
   int U, NUc;
 };
+template <bool SHARED>
 __device__ __forceinline__ StreamSplit stream_split(int H, int C, int cap) {
   StreamSplit sp;
-  sp.U = kDynUnit;
+  sp.U = dyn_unit(SHARED);
   sp.NUc = 0;
   const int per_cta = min(cap / C, kMaxUnitsPerCta);
-  const int dmax = ((H + C - 1) / C) / kDynDiv;
-  if (per_cta > 0 && dmax > 0) {
+  const int dmax = ((H + C - 1) / C) / dyn_div(SHARED);
+  // (SHARED: a part of less than a unit would only add partials)
+  if (per_cta > 0 && dmax >= (SHARED ? sp.U : 1)) {
     if ((dmax + sp.U - 1) / sp.U > per_cta) sp.U = (dmax + per_cta - 1) / per_cta;
     sp.NUc = (dmax + sp.U - 1) / sp.U;
   }
@@ -408,11 +435,12 @@ __device__ __forceinline__ StreamSplit stream_split(int H, int C, int cap) {
 struct Share {
   int x0, y, x1;
 };
+template <bool SHARED>
 __device__ __forceinline__ Share share_of(int c, int H, int C, const StreamSplit& sp) {
   Share sh;
   sh.x0 = share_edge(c, H, C);
   sh.x1 = share_edge(c + 1, H, C);
-  sh.y = sh.x1 - (sp.NUc > 0 ? (sh.x1 - sh.x0) / kDynDiv : 0);
+  sh.y = sh.x1 - (sp.NUc > 0 ? (sh.x1 - sh.x0) / dyn_div(SHARED) : 0);
   return sh;
 }
 
@@ -437,12 +465,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __shared__ int abort_sm;
 
   const int c = blockIdx.x;
-  const int C = gridDim.x;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int NS = p.nstages;
-  const int HB = box_bytes(p.Hkv);              // one TMA box (half of the head dimension)
-  const int SKV = stage_kv_bytes(p.Hkv);        // bytes per stage for K (and for V)
+  constexpr int TS = stage_tokens(SHARED);
+  const int HB = box_bytes(p.Hkv, TS);              // one TMA box (half of the head dimension)
+  const int SKV = stage_kv_bytes(p.Hkv, TS);        // bytes per stage for K (and for V)
   // swizzled TMA destinations must be 1024-byte aligned
   const uint32_t sbase = (smem_u32(dsm_raw) + 1023u) & ~1023u;
   auto full = [&](int st) { return smem_u32(&bars[st]); };
@@ -460,14 +488,23 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // SHARED: the shared-prefix kernel stands in between and lets this one launch only
   // after the scan has finished; its own output is not read here, so this grid starts
   // on every SM that one has left and waits for it at the very end.
-  if constexpr (!SHARED) pdl_wait();
+  // (Where the shared keys are streamed like the others, it does not stand there.)
+  if (!SHARED || !p.pw.together) pdl_wait();
   // The merge kernel may launch once every CTA is past this point, so its launch
   // implies that the scan has finished: it reads the offsets before its own wait.
   pdl_launch_dependents();
-  const int shared = SHARED ? shared_pages(p.pw) : 0;
+  // C: the CTAs with shares of the list
+  int shared = 0, listed = 0, C = gridDim.x;
+  if constexpr (SHARED) {
+    const PrefixSplit ps = prefix_split(p.pw, C);
+    shared = ps.pages;
+    C = ps.own_ctas;
+    if (!p.pw.together) listed = shared_pages(p.pw);   // pages to be read by prefix_table
+  }
   const int H = SHARED ? __ldcg(p.hb + p.B) : p.hb[p.B];
-  const StreamSplit sp = stream_split(H, C, p.dyn_units_cap);
-  const Share own = share_of(c, H, C, sp);
+  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap);
+  Share own = {0, 0, 0};
+  if (c < C) own = share_of<SHARED>(c, H, C, sp);
   __syncthreads();
 
   if (warp >= kConsumerWarps) {
@@ -507,10 +544,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           bq = lo;
           const int hb_b = hbp[bq], hb_n = hbp[bq + 1];
           hh = x - hb_b;
-          const OwnKeys mine = own_keys<SHARED>(p.seq_lens[bq], shared);
-          page = p.block_table[static_cast<size_t>(bq) * p.max_pages + mine.page0 + (hh >> 1)];
+          const int seq = seq_of<SHARED>(p, bq);
+          const OwnKeys mine = own_keys<SHARED>(p.seq_lens[seq], shared);
           len = mine.len;
-          const bool valid = page >= 0 && page < p.num_pages;
+          bool valid;
+          if (SHARED && hh < listed && len >= listed * kPage) {
+            page = p.prefix_table[hh];
+            valid = true;
+            if (page < 0 || page >= p.num_pages) {
+              atomicOr(p.err, kErrBadIndex);
+              page = p.num_pages;                // past the pool: zeros
+            }
+          } else {
+            page = p.block_table[static_cast<size_t>(seq) * p.max_pages + mine.page0 +
+                                 (SHARED ? hh : hh >> 1)];
+            valid = page >= 0 && page < p.num_pages;
+          }
           flags = ((i == 0 || hh == 0) ? 1 : 0) | ((i == cnt - 1 || x + 1 == hb_n) ? 2 : 0) |
                   (valid ? 4 : 0);
         }
@@ -534,13 +583,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
               md.slot0 = slot0;
               meta[st] = md;
               if (kflags & 4) {
-                const int tok0 = kpage * kPage + (khh & 1) * kHalf;
+                const int tok0 = kpage * kPage + (SHARED ? 0 : (khh & 1) * kHalf);
                 const uint32_t kdst = sbase + st * 2 * SKV;
                 mbar_arrive_expect_tx(full(st), 2 * SKV);
-                tma_load_3d(kdst, &tmK, full(st), 0, tok0, 0);
-                tma_load_3d(kdst + HB, &tmK, full(st), 64, tok0, 0);
-                tma_load_3d(kdst + SKV, &tmV, full(st), 0, tok0, 0);
-                tma_load_3d(kdst + SKV + HB, &tmV, full(st), 64, tok0, 0);
+                const int head0 = SHARED ? (kb % p.groups) * p.Hkv : 0;
+                tma_load_3d(kdst, &tmK, full(st), 0, tok0, head0);
+                tma_load_3d(kdst + HB, &tmK, full(st), 64, tok0, head0);
+                tma_load_3d(kdst + SKV, &tmV, full(st), 0, tok0, head0);
+                tma_load_3d(kdst + SKV + HB, &tmV, full(st), 64, tok0, head0);
               } else {
                 atomicOr(p.err, kErrBadIndex);   // consumers skip this stage
                 mbar_arrive(full(st));
@@ -560,7 +610,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       if (lane == 0) u = atomicAdd(p.dyn_next, 1);
       u = __shfl_sync(0xffffffffu, u, 0);
       if (u >= n_units) break;
-      const Share sh = share_of(u / sp.NUc, H, C, sp);
+      const Share sh = share_of<SHARED>(u / sp.NUc, H, C, sp);
       const int xs = sh.y + (u % sp.NUc) * sp.U;
       if (xs < sh.x1) run_range(xs, min(sh.x1, xs + sp.U) - xs, C + p.B + u);
     }
@@ -607,7 +657,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // 32-wide group dg that is swizzled chunk ((dg & 1) * 4 + lane / 8) ^ (lane % 8)
   // in box dg / 2.
   const int lt = lane & 7;
-  const uint32_t row_off = static_cast<uint32_t>((g * kHalf + lt) * 128);
+  const uint32_t row_off = static_cast<uint32_t>((g * TS + lt) * 128);
   uint32_t ld_off[4];
 #pragma unroll
   for (int dg = 0; dg < 4; ++dg)
@@ -634,31 +684,47 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int nn = 0; nn < 16; ++nn) o[nn][0] = o[nn][1] = o[nn][2] = o[nn][3] = 0.f;
       }
       if (md.flags & 4) {
-        const int ntok = min(kHalf, md.len - md.hh * kHalf);
+        const int ntok = min(TS, md.len - md.hh * TS);
         const uint32_t kaddr = sbase + st * 2 * SKV;
         const uint32_t vaddr = kaddr + SKV;
-        // S = Q K^T over the 128-wide head dimension, 32 columns per ldmatrix
-        float sa[4] = {0.f, 0.f, 0.f, 0.f};
+        // S = Q K^T over the 128-wide head dimension, 32 columns per ldmatrix; eight
+        // tokens (1024 bytes on) to a score tile
+        constexpr int TILES = TS / kHalf;
+        float sa[TILES][4] = {};
 #pragma unroll
         for (int dg = 0; dg < 4; ++dg) {
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(kaddr + ld_off[dg], b0, b1, b2, b3);
-          mma_bf16_16816(sa, qa[2 * dg][0], 0u, qa[2 * dg][1], 0u, b0, b1);
-          mma_bf16_16816(sa, qa[2 * dg + 1][0], 0u, qa[2 * dg + 1][1], 0u, b2, b3);
+#pragma unroll
+          for (int tt = 0; tt < TILES; ++tt) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(kaddr + ld_off[dg] + tt * kHalf * 128, b0, b1, b2, b3);
+            mma_bf16_16816(sa[tt], qa[2 * dg][0], 0u, qa[2 * dg][1], 0u, b0, b1);
+            mma_bf16_16816(sa[tt], qa[2 * dg + 1][0], 0u, qa[2 * dg + 1][1], 0u, b2, b3);
+          }
         }
         const int t0 = 2 * tq;
-        const float s0 = t0 < ntok ? sa[0] * p.scale_log2 : -INFINITY;
-        const float s1 = t0 + 1 < ntok ? sa[1] * p.scale_log2 : -INFINITY;
-        float mx = fmaxf(s0, s1);
+        float sc[TILES][2];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int tt = 0; tt < TILES; ++tt) {
+          sc[tt][0] = tt * kHalf + t0 < ntok ? sa[tt][0] * p.scale_log2 : -INFINITY;
+          sc[tt][1] = tt * kHalf + t0 + 1 < ntok ? sa[tt][1] * p.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, fmaxf(sc[tt][0], sc[tt][1]));
+        }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float m_new = fmaxf(m_run, mx);
         const float alpha = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
         m_run = m_new;
-        const float p0 = (s0 == -INFINITY) ? 0.f : ex2(s0 - m_run);
-        const float p1 = (s1 == -INFINITY) ? 0.f : ex2(s1 - m_run);
-        l_run = l_run * alpha + (p0 + p1);
-        const uint32_t pa = pack_bf16x2(p0, p1);   // P A-fragment: row gq, tokens 2 tq, 2 tq + 1
+        float psum = 0.f;
+        uint32_t pa[TILES];                      // P A-fragments: row gq, tokens 2 tq, 2 tq + 1
+#pragma unroll
+        for (int tt = 0; tt < TILES; ++tt) {
+          const float p0 = (sc[tt][0] == -INFINITY) ? 0.f : ex2(sc[tt][0] - m_run);
+          const float p1 = (sc[tt][1] == -INFINITY) ? 0.f : ex2(sc[tt][1] - m_run);
+          psum += p0 + p1;
+          pa[tt] = pack_bf16x2(p0, p1);
+        }
+        l_run = l_run * alpha + psum;
 #pragma unroll
         for (int nn = 0; nn < 16; ++nn) {
           o[nn][0] *= alpha;
@@ -666,21 +732,30 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         // slots behind the sequence's last token hold whatever the pool held: their
         // weights are zero, and so must their values be (zero times NaN is NaN)
-        const uint32_t v_keep = (t0 < ntok ? 0x0000ffffu : 0u) | (t0 + 1 < ntok ? 0xffff0000u : 0u);
+        uint32_t v_keep[TILES];
+#pragma unroll
+        for (int tt = 0; tt < TILES; ++tt)
+          v_keep[tt] = (tt * kHalf + t0 < ntok ? 0x0000ffffu : 0u) |
+                       (tt * kHalf + t0 + 1 < ntok ? 0xffff0000u : 0u);
 #pragma unroll
         for (int ng = 0; ng < 4; ++ng) {
-          uint32_t v0, v1, v2, v3;
-          ldsm_x4_t(vaddr + ld_off[ng], v0, v1, v2, v3);
-          if (ntok < kHalf) {
-            v0 &= v_keep;
-            v1 &= v_keep;
-            v2 &= v_keep;
-            v3 &= v_keep;
+          uint32_t v[TILES][4];
+#pragma unroll
+          for (int tt = 0; tt < TILES; ++tt) {
+            ldsm_x4_t(vaddr + ld_off[ng] + tt * kHalf * 128, v[tt][0], v[tt][1], v[tt][2],
+                      v[tt][3]);
+            if (ntok < TS) {
+#pragma unroll
+              for (int i4 = 0; i4 < 4; ++i4) v[tt][i4] &= v_keep[tt];
+            }
           }
-          mma_bf16_1688(o[4 * ng + 0], pa, 0u, v0);
-          mma_bf16_1688(o[4 * ng + 1], pa, 0u, v1);
-          mma_bf16_1688(o[4 * ng + 2], pa, 0u, v2);
-          mma_bf16_1688(o[4 * ng + 3], pa, 0u, v3);
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            if constexpr (TILES == 2)
+              mma_bf16_16816(o[4 * ng + i4], pa[0], 0u, pa[1], 0u, v[0][i4], v[1][i4]);
+            else
+              mma_bf16_1688(o[4 * ng + i4], pa[0], 0u, v[0][i4]);
+          }
         }
       }
 
@@ -718,13 +793,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // kMergeBatch partial rows of a head in one round of independent loads.
 constexpr int kMergeBatch = 8;
 
-// Joins n partial results of one (sequence, query head) by their LSE: lse_at(k) and
+// n partial results of one (sequence, query head) joined by their LSE: lse_at(k) and
 // row_at(k) (the lane's four columns) give the k-th.  32 partials at a time (one
 // sequence rarely has more): one LSE per lane and the first kMergeBatch rows load
 // together; a later chunk with a larger maximum rescales what is accumulated so far.
+struct Joined {
+  float4 acc;       // the lane's columns, weighted by exp(LSE - mx)
+  float wsum, mx;   // sum of the weights (all lanes), their reference
+};
 template <class LseAt, class RowAt>
-__device__ __forceinline__ void merge_head(int n, int lane, LseAt lse_at, RowAt row_at,
-                                           uint16_t* o, float* lse) {
+__device__ __forceinline__ Joined join_partials(int n, int lane, LseAt lse_at, RowAt row_at) {
   float wsum = 0.f, mx = -INFINITY;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < n; k0 += 32) {
@@ -768,10 +846,13 @@ __device__ __forceinline__ void merge_head(int n, int lane, LseAt lse_at, RowAt 
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  *reinterpret_cast<uint2*>(o + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lse && lane == 0) *lse = wsum > 0.f ? mx + __log2f(wsum) * kLn2 : -INFINITY;
+  return {acc, wsum, mx};
+}
+__device__ __forceinline__ void store_joined(const Joined& r, int lane, uint16_t* o, float* lse) {
+  const float inv = r.wsum > 0.f ? 1.f / r.wsum : 0.f;
+  *reinterpret_cast<uint2*>(o + lane * 4) = make_uint2(
+      pack_bf16x2(r.acc.x * inv, r.acc.y * inv), pack_bf16x2(r.acc.z * inv, r.acc.w * inv));
+  if (lse && lane == 0) *lse = r.wsum > 0.f ? r.mx + __log2f(r.wsum) * kLn2 : -INFINITY;
 }
 
 // The segments of the shared prefix that hold row (b, h): n of them, the k-th at row
@@ -783,8 +864,8 @@ struct PrefixRows {
 __device__ __forceinline__ PrefixRows prefix_rows(const DecodeParams& p, const PrefixSplit& sp,
                                                   int b, int h) {
   const int G = p.Hq / p.Hkv;
-  const int row = b * G + h % G;
-  const int item = (h / G) * p.pw.pairs + (row >> 8);
+  const int row = b / p.groups * G + h % G;
+  const int item = (b % p.groups * p.Hkv + h / G) * p.pw.pairs + (row >> 8);
   const int c0 = cta_of(static_cast<long long>(item) * sp.nt, sp.units, sp.ctas);
   const int c1 = cta_of(static_cast<long long>(item + 1) * sp.nt - 1, sp.units, sp.ctas);
   PrefixRows r;
@@ -793,9 +874,19 @@ __device__ __forceinline__ PrefixRows prefix_rows(const DecodeParams& p, const P
   return r;
 }
 
+// SHARED: blocks of 8 warps, `p.merge_split` of which share a row's partials, so that few
+// rows with many partials (a long prefix, a small batch) use more warps than they are: as
+// many as keep all warps resident.  Two sequences of 1024 pages, 32 + 8 heads: 33.9 us a
+// warp a row, 29.8 us so; 7 sequences of 65 pages, 8 + 2 heads: 15.2 and 13.0 us.
 template <bool SHARED>
-__global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kernel(
+__global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_merge_kernel(
     const DecodeParams p) {
+  constexpr int kWarps = merge_warps(SHARED);
+  const int split = SHARED ? p.merge_split : 1;
+  const int rows = kWarps / split;             // heads of the block at a time
+  const int head_step = SHARED ? gridDim.y * rows : kWarps;
+  const int head0 = SHARED ? blockIdx.y * rows : 0;
+  __shared__ Joined parts[SHARED ? kWarps : 1][32];
   __shared__ int slots[kMaxMergeSlots];
   __shared__ int n_slots_sm;
   const int b = blockIdx.x;
@@ -806,11 +897,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
   bool sees = false;                           // the sequence has the shared keys
   if constexpr (SHARED) {
     ps = prefix_split(p.pw, p.pw.ctas);
-    sees = ps.pages > 0 && checked_len(p, b) >= ps.pages * kPage;
+    sees = ps.pages > 0 && checked_len(p, seq_of<SHARED>(p, b)) >= ps.pages * kPage;
   }
   if (xe <= xs && !sees) {                     // no keys (or an invalid length): O = 0, LSE = -inf
     pdl_wait();
-    for (int h = warp; h < p.Hq; h += kMergeWarps) {
+    for (int h = head0 + warp; warp < rows && h < p.Hq; h += head_step) {
       const size_t wid = static_cast<size_t>(b) * p.Hq + h;
       *reinterpret_cast<uint2*>(p.o + wid * kDecD + lane * 4) = make_uint2(0, 0);
       if (p.lse && lane == 0) p.lse[wid] = -INFINITY;
@@ -818,8 +909,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
     return;
   }
   const int H = __ldcg(p.hb + p.B);
-  const int C = p.nctas;
-  const StreamSplit sp = stream_split(H, C, p.dyn_units_cap);
+  const int C = SHARED ? ps.own_ctas : p.nctas;
+  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap);
   if (warp == 0) {
     int base = 0;
     // no own keys: an empty range
@@ -830,7 +921,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
       Share sh;
       int own = 0, k0 = 0, k1 = -1;
       if (cc <= c_last) {
-        sh = share_of(cc, H, C, sp);
+        sh = share_of<SHARED>(cc, H, C, sp);
         own = max(xs, sh.x0) < min(xe, sh.y) ? 1 : 0;
         const int lo = max(xs, sh.y), hi = min(xe, sh.x1);
         if (lo < hi) {
@@ -859,59 +950,54 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_decode_stream_merge_kerne
   pdl_wait();                                  // the stream kernel's partials
   const float4* wo = reinterpret_cast<const float4*>(p.ws_o);
   const float4* po = reinterpret_cast<const float4*>(p.pre_o);
-  for (int h = warp; h < p.Hq; h += kMergeWarps) {
-    PrefixRows pr;
-    pr.n = 0;
-    pr.row0 = 0;
-    if (SHARED && sees) pr = prefix_rows(p, ps, b, h);
+  const int share = SHARED ? warp % split : 0; // partials share, share + split, ... are the warp's
+  for (int h0 = head0; h0 < p.Hq; h0 += head_step) {
+    const int h = h0 + (SHARED ? warp / split : warp);
     const size_t wid = static_cast<size_t>(b) * p.Hq + h;
-    merge_head(
-        ns + pr.n, lane,
-        [&](int k) {
-          if (SHARED && k >= ns) return __ldcg(p.pre_lse + pr.row0 + static_cast<size_t>(k - ns) * 256);
-          return __ldcg(p.ws_lse + static_cast<size_t>(slots[k]) * p.Hq + h);
-        },
-        [&](int k) {
-          if (SHARED && k >= ns)
-            return __ldcg(po + (pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane);
-          return __ldcg(wo + (static_cast<size_t>(slots[k]) * p.Hq + h) * (kDecD / 4) + lane);
-        },
-        p.o + wid * kDecD, p.lse ? p.lse + wid : nullptr);
+    Joined r = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f, -INFINITY};
+    if (h < p.Hq) {
+      PrefixRows pr;
+      pr.n = 0;
+      pr.row0 = 0;
+      if (SHARED && sees) pr = prefix_rows(p, ps, b, h);
+      r = join_partials(
+          (ns + pr.n - share + split - 1) / split, lane,
+          [&](int k) {
+            if (SHARED) k = share + k * split;
+            if (SHARED && k >= ns)
+              return __ldcg(p.pre_lse + pr.row0 + static_cast<size_t>(k - ns) * 256);
+            return __ldcg(p.ws_lse + static_cast<size_t>(slots[k]) * p.Hq + h);
+          },
+          [&](int k) {
+            if (SHARED) k = share + k * split;
+            if (SHARED && k >= ns)
+              return __ldcg(po + (pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane);
+            return __ldcg(wo + (static_cast<size_t>(slots[k]) * p.Hq + h) * (kDecD / 4) + lane);
+          });
+    }
+    if (SHARED && split > 1) {
+      parts[warp][lane] = r;
+      __syncthreads();
+      if (share == 0) {
+        float mx = r.mx;
+        for (int i = 1; i < split; ++i) mx = fmaxf(mx, parts[warp + i][lane].mx);
+        Joined all = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f, mx};
+        for (int i = 0; i < split; ++i) {
+          const Joined q = parts[warp + i][lane];
+          const float w = q.mx == -INFINITY ? 0.f : ex2((q.mx - mx) * kLog2e);
+          all.acc.x = fmaf(w, q.acc.x, all.acc.x);
+          all.acc.y = fmaf(w, q.acc.y, all.acc.y);
+          all.acc.z = fmaf(w, q.acc.z, all.acc.z);
+          all.acc.w = fmaf(w, q.acc.w, all.acc.w);
+          all.wsum = fmaf(w, q.wsum, all.wsum);
+        }
+        r = all;
+      }
+      __syncthreads();                         // read before the next heads' are written
+    }
+    if (h < p.Hq && share == 0)
+      store_joined(r, lane, p.o + wid * kDecD, p.lse ? p.lse + wid : nullptr);
   }
-}
-
-// SHARED, direct schedule: joins the chunks of a sequence's own keys and the segments of
-// the shared prefix; a warp per (sequence, query head).
-__global__ void __launch_bounds__(kDecThreads) fa_decode_shared_combine_kernel(
-    const DecodeParams p) {
-  const long long bh = static_cast<long long>(blockIdx.x) * kDecWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (bh >= static_cast<long long>(p.B) * p.Hq) return;
-  const int b = static_cast<int>(bh / p.Hq);
-  const int h = static_cast<int>(bh - static_cast<long long>(b) * p.Hq);
-  const PrefixSplit ps = prefix_split(p.pw, p.pw.ctas);
-  const int seq_len = checked_len(p, b);
-  const int len = own_keys<true>(seq_len, ps.pages).len;
-  const int npages = len > 0 ? (len + kPage - 1) / kPage : 0;
-  const int ns = (npages + p.pps - 1) / p.pps;
-  PrefixRows pr;
-  pr.n = 0;
-  pr.row0 = 0;
-  if (ps.pages > 0 && seq_len >= ps.pages * kPage) pr = prefix_rows(p, ps, b, h);
-  const float4* wo = reinterpret_cast<const float4*>(p.ws_o);
-  const float4* po = reinterpret_cast<const float4*>(p.pre_o);
-  const size_t base = static_cast<size_t>(b) * p.nsplit * p.Hq + h;
-  merge_head(
-      ns + pr.n, lane,
-      [&](int k) {
-        return k >= ns ? p.pre_lse[pr.row0 + static_cast<size_t>(k - ns) * 256]
-                       : p.ws_lse[base + static_cast<size_t>(k) * p.Hq];
-      },
-      [&](int k) {
-        return k >= ns ? po[(pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane]
-                       : wo[(base + static_cast<size_t>(k) * p.Hq) * (kDecD / 4) + lane];
-      },
-      p.o + bh * kDecD, p.lse ? p.lse + bh : nullptr);
 }
 
 // One CTA of 128 threads per (sequence, query head); thread d owns output column d.
@@ -988,6 +1074,7 @@ int sm_count(int device) {
 // The shared prefix of a SHARED call: its page ids, how its work is split, and the
 // workspace of its segments.
 struct SharedPrefix {
+  int B = 0, Hq = 0, Hkv = 0, groups = 1;      // of the call; head groups of a sequence
   const int32_t* table = nullptr;
   PrefixWork work;
   float* ws_o = nullptr;
@@ -1025,17 +1112,19 @@ void finish_plan(DecodePlan& pl, int B, int Hq, int Hkv) {
   }
 }
 
-DecodePlan make_plan(int B, int Hq, int Hkv, int max_pages_per_seq, int nsm) {
+DecodePlan make_plan(int B, int Hq, int Hkv, int max_pages_per_seq, int nsm,
+                     bool shared = false) {
   DecodePlan pl;
   // streamed: one consumer warp per KV head, its G <= 8 query heads as MMA rows
   pl.streamed = Hkv <= kDecWarps && nsm > 0;
   if (pl.streamed) {
     pl.nctas = std::min(nsm, kMaxStreamCtas);
-    pl.nstages = kStreamSmemBudget / (2 * stage_kv_bytes(Hkv));
+    pl.nstages = kStreamSmemBudget / (2 * stage_kv_bytes(Hkv, stage_tokens(shared)));
     if (pl.nstages > kMaxStages) pl.nstages = kMaxStages;
     // enough units for the dynamic part of every share of the longest possible list
     const long long h_max = 2LL * B * max_pages_per_seq;
-    const long long per_cta = ((h_max + pl.nctas - 1) / pl.nctas) / kDynDiv / kDynUnit + 1;
+    const long long per_cta =
+        ((h_max + pl.nctas - 1) / pl.nctas) / dyn_div(shared) / dyn_unit(shared) + 1;
     pl.dyn_units_cap = static_cast<int>(std::min<long long>(per_cta * pl.nctas, 1 << 24));
   } else {
     pl.pps = direct_pps(B, max_pages_per_seq);
@@ -1049,14 +1138,8 @@ template <int G, bool SHARED>
 int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensorMap& tmK,
                    const CUtensorMap& tmV, const SharedPrefix* pre, cudaStream_t stream,
                    int device) {
-  // The shared prefix comes right after the scan (streamed: overlapping it and the
-  // stream kernel) or first of all (direct).
-  auto prefix = [&](bool overlap) {
-    return launch_prefix(prm.q, prm.kc, prm.vc, prm.pw, pre->table, pre->ws_o, pre->ws_lse, prm.B,
-                         prm.Hq, prm.Hkv, prm.num_pages, pre->scale, overlap, stream, device);
-  };
   if (pl.streamed) {
-    const int smem = pl.nstages * 2 * stage_kv_bytes(prm.Hkv) + 1024 +
+    const int smem = pl.nstages * 2 * stage_kv_bytes(prm.Hkv, stage_tokens(SHARED)) + 1024 +
                      (prm.hb_in_smem ? (prm.B + 1) * 4 : 0);
     {
       // the shared-memory limit is a property of the function on each device
@@ -1085,29 +1168,27 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
     cfg.numAttrs = 1;
     fa_decode_scan_kernel<SHARED><<<1, 1024, 0, stream>>>(prm);
     if constexpr (SHARED) {
-      const int rc = prefix(true);
-      if (rc != FA_OK) return rc;
+      // right after the scan, overlapping it and the stream kernel
+      if (prm.pw.together) {
+        const int rc = launch_prefix(prm.q, prm.kc, prm.vc, prm.pw, pre->table, pre->ws_o,
+                                     pre->ws_lse, pre->B, pre->Hq, pre->Hkv, prm.num_pages,
+                                     pre->scale, stream, device);
+        if (rc != FA_OK) return rc;
+      }
     }
     cfg.gridDim = dim3(pl.nctas);
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchKernelEx(&cfg, fa_decode_stream_kernel<G, SHARED>, tmK, tmV, prm);
-    cfg.gridDim = dim3(prm.B);
-    cfg.blockDim = dim3(kMergeWarps * 32);
+    constexpr int mw = merge_warps(SHARED);
+    cfg.gridDim = dim3(prm.B, SHARED ? (prm.Hq * prm.merge_split + mw - 1) / mw : 1);
+    cfg.blockDim = dim3(mw * 32);
     cfg.dynamicSmemBytes = 0;
     cudaLaunchKernelEx(&cfg, fa_decode_stream_merge_kernel<SHARED>, prm);
-  } else {
-    if constexpr (SHARED) {
-      const int rc = prefix(false);
-      if (rc != FA_OK) return rc;
-    }
+  } else if constexpr (!SHARED) {
     dim3 grid(pl.nsplit, prm.B);
-    fa_decode_split_kernel<G, SHARED><<<grid, kDecThreads, 0, stream>>>(prm);
-    if constexpr (SHARED)
-      fa_decode_shared_combine_kernel<<<(prm.B * prm.Hq + kDecWarps - 1) / kDecWarps, kDecThreads,
-                                        0, stream>>>(prm);
-    else
-      fa_decode_combine_kernel<<<prm.B * prm.Hq, kDecD, 0, stream>>>(prm);
+    fa_decode_split_kernel<G><<<grid, kDecThreads, 0, stream>>>(prm);
+    fa_decode_combine_kernel<<<prm.B * prm.Hq, kDecD, 0, stream>>>(prm);
   }
   return FA_OK;
 }
@@ -1140,8 +1221,13 @@ int run_decode(const void* q, const void* kcache, const void* vcache, const int3
   prm.scale_log2 = scale * kLog2e;
   prm.err = device_error_word(device);
   if (!prm.err) return set_error(FA_ERR_CUDA, "device error word unavailable");
+  prm.groups = pre ? pre->groups : 1;
+  prm.merge_split = 1;
+  while (pre && prm.merge_split < 8 && 2LL * prm.merge_split * B * Hq <= 8LL * 3 * pl.nctas)
+    prm.merge_split *= 2;
   prm.pw = PrefixWork{};
   prm.pre_o = prm.pre_lse = nullptr;
+  prm.prefix_table = pre ? pre->table : nullptr;
   if (pre) {
     prm.pw = pre->work;
     prm.pw.err = prm.err;
@@ -1155,16 +1241,18 @@ int run_decode(const void* q, const void* kcache, const void* vcache, const int3
   prm.ws_o = static_cast<float*>(ws);
   prm.ws_lse = prm.ws_o + pl.n_part * kDecD;
   prm.hb = reinterpret_cast<int*>(prm.ws_lse + pl.n_part);
+  prm.pw.own_total = prm.hb + B;
   prm.dyn_next = prm.hb + (B + 1);
   CUtensorMap tmK, tmV;
   if (pl.streamed) {
     // K and V caches viewed as [Hkv][num_pages * 16 tokens][128]: box {64, 8, Hkv}
     const uint64_t dims[3] = {static_cast<uint64_t>(kDecD),
                               static_cast<uint64_t>(num_pages) * kPage,
-                              static_cast<uint64_t>(Hkv)};
-    const uint64_t strides[2] = {static_cast<uint64_t>(Hkv) * kDecD * 2,
+                              static_cast<uint64_t>(Hkv) * prm.groups};
+    const uint64_t strides[2] = {static_cast<uint64_t>(Hkv) * prm.groups * kDecD * 2,
                                  static_cast<uint64_t>(kDecD) * 2};
-    const uint32_t box[3] = {64, static_cast<uint32_t>(kHalf), static_cast<uint32_t>(Hkv)};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(stage_tokens(pre != nullptr)),
+                             static_cast<uint32_t>(Hkv)};
     int rc = encode_tensor_map_16bit(&tmK, kcache, true, 3, dims, strides, box);
     if (rc == FA_OK) rc = encode_tensor_map_16bit(&tmV, vcache, true, 3, dims, strides, box);
     if (rc != FA_OK) return rc;
@@ -1228,13 +1316,20 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   const int G = Hq / Hkv;
   const int nsm = sm_count(device);
   if (nsm <= 0) return set_error(FA_ERR_CUDA, "cannot read the SM count of device %d", device);
-  DecodePlan pl = make_plan(B, Hq, Hkv, max_pages_per_seq, nsm);
-  if (pl.streamed) {
-    // a CTA never gets more units than this, so no more slots are needed either
-    pl.dyn_units_cap = std::min(pl.dyn_units_cap, pl.nctas * kMaxUnitsPerCta);
-    finish_plan(pl, B, Hq, Hkv);
-  }
   SharedPrefix pre;
+  pre.B = B;
+  pre.Hq = Hq;
+  pre.Hkv = Hkv;
+  while (Hkv % pre.groups != 0 || Hkv / pre.groups > kConsumerWarps) ++pre.groups;
+  const int gq = Hq / pre.groups, gkv = Hkv / pre.groups;
+  const long long entries = static_cast<long long>(B) * pre.groups;
+  if (2 * entries * max_pages_per_seq > 0x7fffffffLL)
+    return set_error(FA_ERR_UNSUPPORTED, "shared prefix: too many keys for one call");
+  const int gb = static_cast<int>(entries);
+  DecodePlan pl = make_plan(gb, gq, gkv, max_pages_per_seq, nsm, true);
+  // a CTA never gets more units than this, so no more slots are needed either
+  pl.dyn_units_cap = std::min(pl.dyn_units_cap, pl.nctas * kMaxUnitsPerCta);
+  finish_plan(pl, gb, gq, gkv);
   pre.table = prefix_table;
   pre.scale = scale;
   pre.work.pages = prefix_pages;
@@ -1247,9 +1342,20 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
     return set_error(FA_ERR_UNSUPPORTED, "shared prefix: too much work for one call");
   pre.work.pairs = static_cast<int>(pairs);
   pre.work.items = static_cast<int>(items);
+  // Few copies of few shared pages are streamed with the own ones: the copies come from L2,
+  // and the prefix kernel's start and end cost about 7 us.  32 + 8 heads, together / apart:
+  // 7 sequences of 32 pages 17.2 / 13.8 us, of 130 19.0 / 17.3, of 260 20.3 / 22.2;
+  // 64 of 16 19.5 / 18.6, of 32 20.2 / 26.7.
+  pre.work.together = entries * max_prefix_pages > 1024;
+  // Measured on an SM: a key tile against two row tiles 1.9 to 2.3 us, against one 1.8 us;
+  // a page of 8 KV heads 0.92 us.  What matters is their ratio.  us of 256 sequences with
+  // 32768 shared keys / 64 with 4096 at 2050 and 350 ns: 318 / 106, 700: 181 / 106, 1000:
+  // 170 / 107, 1400: 178 / 126, 2000: 190 / 150, 3000: 219 / 199.
+  pre.work.tile_ns = static_cast<long long>(B) * G > 128 ? 2050 : 1800;
+  pre.work.page_ns = 950;
   pre.work.ctas = nsm;
   // segments write to slot CTA + item
-  const size_t pre_rows = static_cast<size_t>(nsm + items) * 256;
+  const size_t pre_rows = pre.work.together ? static_cast<size_t>(nsm + items) * 256 : 0;
   const size_t pre_bytes = (pre_rows * (kDecD + 1) * sizeof(float) + 255) & ~size_t(255);
   cudaMemPool_t pool;
   int rc = get_pool(device, &pool);
@@ -1261,8 +1367,9 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
                      cudaGetErrorString(e));
   pre.ws_o = static_cast<float*>(ws);
   pre.ws_lse = pre.ws_o + pre_rows * kDecD;
-  rc = run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, max_pages_per_seq,
-                  num_pages, scale, pl, static_cast<char*>(ws) + pre_bytes, stream, device, &pre);
+  rc = run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, gb, gq, gkv,
+                  max_pages_per_seq, num_pages, scale, pl, static_cast<char*>(ws) + pre_bytes,
+                  stream, device, &pre);
   cudaError_t ef = cudaFreeAsync(ws, stream);
   if (rc != FA_OK) return rc;
   if (ef != cudaSuccess)

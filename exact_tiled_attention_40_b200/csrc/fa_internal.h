@@ -141,18 +141,24 @@ int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device);
 
 // Shared-prefix attention: how its work is split (see prefix_split.cuh).
 constexpr int kPrefixTile = 128;        // keys per tile
-constexpr int kPrefixMinTiles = 2;      // key tiles that a CTA takes at least
+// Pages that a CTA streams at least: fewer make more partials than they save time (us with
+// 2 / 3 / 4: 2 sequences of 64 pages 17.0 / 15.5 / 16.0, 16 of 16 14.7 / 13.8 / 14.5).
+constexpr int kOwnMinPages = 3;
 struct PrefixWork {
   const int32_t* pages = nullptr;       // number of shared pages, on the device
+  const int* own_total = nullptr;       // pages that are streamed, on the device (the scan's sum)
   int max_pages = 0;                    // bound on it
+  bool together = true;                 // attended for the whole batch at once
   int pairs = 0;                        // 256-row pairs of a KV head's B * G rows
   int items = 0;                        // Hkv * pairs
-  int ctas = 0;                         // grid of the prefix kernel
+  int tile_ns = 0;                      // estimated time of a key tile of a pair on an SM
+  int page_ns = 0;                      // of a streamed page
+  int ctas = 0;                         // grid of the prefix and of the stream kernel
   int* err = nullptr;
 };
 int launch_prefix(const void* q, const void* kcache, const void* vcache, const PrefixWork& w,
                   const int32_t* prefix_table, float* ws_o, float* ws_lse, int B, int Hq, int Hkv,
-                  int num_pages, float scale, bool overlap, cudaStream_t stream, int device);
+                  int num_pages, float scale, cudaStream_t stream, int device);
 int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
                          const int32_t* block_table, const int32_t* seq_lens,
                          const int32_t* prefix_table, const int32_t* prefix_pages,

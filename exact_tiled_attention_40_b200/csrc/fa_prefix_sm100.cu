@@ -7,18 +7,24 @@
 // 4 * B * Hq * 128 flops against 4 * 128 * Hkv bytes, so a batch of a few dozen rows a
 // KV head is bound by HBM and one of a few hundred by the tensor cores.
 //
-// The work is a list of (KV head, pair of 128-row tiles, 128-key tile) units; CTA c
-// takes the equal contiguous share [c W / C, (c + 1) W / C) of its W units, whatever
-// the prefix length, so that few rows over a long prefix still use every SM.  A share
-// that spans several (head, pair) items is cut into segments; every segment writes its
-// normalised partial output and LSE in fp32 to slot c + item (unique: along the list c,
-// item or both grow by one), and the decode merge joins a row's segments with the
-// partials of its own keys by their LSE.
+// The work is a list of (KV head, pair of 128-row tiles, 128-key tile) units; of the C CTAs
+// that prefix_split.cuh gives it, CTA c takes the equal contiguous share
+// [c W / C, (c + 1) W / C) of its W units, whatever the prefix length, so that few rows over
+// a long prefix still use every SM.  A share that spans several (head, pair) items is cut
+// into segments; every segment writes its normalised partial output and LSE in fp32 to slot
+// c + item (unique: along the list c, item or both grow by one), and the decode merge joins
+// a row's segments with the partials of its own keys by their LSE.
 //
 // Within a segment this is the online-softmax pipeline of the forward kernel on
 // tcgen05 (see there for the roles and the tensor-memory plan): a producer warp gathers
 // the 16-token pages of K and V by TMA into a ring of four 128-key tiles, one warp
 // issues S = Q K^T and O += P V, two softmax warpgroups own a row tile each.
+//
+// 256 sequences of 32 + 8 heads over 37888 shared keys (1024 rows a KV head, 158 GFLOP):
+// 146 us, 1085 TFLOP/s; from one key count to the next 2.0 us a unit, the forward kernel's
+// rate, and 18 us for two segments' starts and ends.  With every page id the same (L2)
+// 140 us: the chain of S, softmax and P V bounds it, not memory.  33 rows a KV head, 16
+// heads: 1.8 us a unit (one row tile), 5.4 TB/s.
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -139,7 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // Everything above overlaps the scan of the lengths; its sum decides the split.
+  pdl_wait();
   const PrefixSplit sp = prefix_split(p.w, C);
+  // The next kernel of the stream reads the scan's output without waiting for this grid:
+  // the scan has finished.
+  pdl_launch_dependents();
   const int pages = sp.pages;
   const int n_keys = pages * kPageTok;
   tc_fence_before();
@@ -326,11 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(mma_done);
       volatile int no_abort = 0;
       mbar_wait(mma_done, 0, &no_abort, p.err, p.timeout_ns);
-    } else if (warp == 10 && lane == 0) {
-      // The next kernel of the stream reads the scan's output without waiting for this
-      // grid: let it launch only once the scan has finished.
-      pdl_wait();
-      pdl_launch_dependents();
     }
   } else {
     regs_inc<kRegsSoftmax>();
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int launch_prefix(const void* q, const void* kcache, const void* vcache, const PrefixWork& w,
                   const int32_t* prefix_table, float* ws_o, float* ws_lse, int B, int Hq, int Hkv,
-                  int num_pages, float scale, bool overlap, cudaStream_t stream, int device) {
+                  int num_pages, float scale, cudaStream_t stream, int device) {
   const int G = Hq / Hkv;
   int rc = raise_smem_limit(reinterpret_cast<const void*>(fa_prefix_kernel), kSmemBytes, device,
                             kSmemPrefix);
@@ -530,7 +536,7 @@ int launch_prefix(const void* q, const void* kcache, const void* vcache, const P
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = pdl;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel, tq, tk, tv, prm);
   if (e != cudaSuccess)
     return set_error(FA_ERR_CUDA, "shared-prefix launch: %s", cudaGetErrorString(e));

@@ -36,18 +36,29 @@ __device__ __forceinline__ int shared_pages(const PrefixWork& w) {
   return n;
 }
 
+// The prefix kernel and the stream kernel are both bound by what an SM does (tiles, pages),
+// so the SMs are divided between them in proportion to their work: `ctas` of the C take
+// prefix tiles, and the stream kernel's first C - ctas blocks, which start at once on the
+// others, share the sequences' own pages.
 struct PrefixSplit {
-  int pages;       // shared pages
+  int pages;       // shared pages that are attended at once
   int nt;          // key tiles of the prefix
   int units;       // items * nt
-  int ctas;        // CTAs that take a share (0: no prefix)
+  int ctas;        // CTAs that take a share of the units (0: no prefix)
+  int own_ctas;    // CTAs that take a share of the streamed pages (1 to C)
 };
+// Read after the scan of the lengths has finished.
 __device__ __forceinline__ PrefixSplit prefix_split(const PrefixWork& w, int C) {
   PrefixSplit s;
-  s.pages = shared_pages(w);
+  s.pages = w.together ? shared_pages(w) : 0;
   s.nt = (s.pages * 16 + kPrefixTile - 1) / kPrefixTile;
   s.units = w.items * s.nt;
-  s.ctas = min(C, (s.units + kPrefixMinTiles - 1) / kPrefixMinTiles);
+  const long long prefix = static_cast<long long>(s.units) * w.tile_ns;
+  const int own_pages = __ldcg(w.own_total);
+  const long long own = static_cast<long long>(own_pages) * w.page_ns;
+  s.ctas = s.units == 0 ? 0 : static_cast<int>(min((prefix * C + prefix + own - 1) / (prefix + own),
+                                                   static_cast<long long>(min(C, s.units))));
+  s.own_ctas = min(s.ctas < C ? C - s.ctas : C, max(1, own_pages / kOwnMinPages));
   return s;
 }
 
