@@ -856,21 +856,23 @@ __device__ __forceinline__ void store_joined(const Joined& r, int lane, uint16_t
 }
 
 // The segments of the shared prefix that hold row (b, h): n of them, the k-th at row
-// row0 + 256 k of the segments' workspace.
+// row0 + k step of the segments' workspace.
 struct PrefixRows {
   int n;
-  size_t row0;
+  size_t row0, step;
 };
 __device__ __forceinline__ PrefixRows prefix_rows(const DecodeParams& p, const PrefixSplit& sp,
                                                   int b, int h) {
   const int G = p.Hq / p.Hkv;
   const int row = b / p.groups * G + h % G;
-  const int item = (b % p.groups * p.Hkv + h / G) * p.pw.pairs + (row >> 8);
-  const int c0 = cta_of(static_cast<long long>(item) * sp.nt, sp.units, sp.ctas);
-  const int c1 = cta_of(static_cast<long long>(item + 1) * sp.nt - 1, sp.units, sp.ctas);
+  const int group = (row >> 8) / p.pw.team, member = (row >> 8) - group * p.pw.team;
+  const int item = (b % p.groups * p.Hkv + h / G) * p.pw.pair_groups + group;
+  const int c0 = cta_of(static_cast<long long>(item) * sp.nt, sp.units, sp.teams);
+  const int c1 = cta_of(static_cast<long long>(item + 1) * sp.nt - 1, sp.units, sp.teams);
   PrefixRows r;
   r.n = c1 - c0 + 1;
-  r.row0 = static_cast<size_t>(c0 + item) * 256 + (row & 255);
+  r.row0 = (static_cast<size_t>(c0 + item) * p.pw.team + member) * 256 + (row & 255);
+  r.step = static_cast<size_t>(p.pw.team) * 256;
   return r;
 }
 
@@ -958,20 +960,20 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
     if (h < p.Hq) {
       PrefixRows pr;
       pr.n = 0;
-      pr.row0 = 0;
+      pr.row0 = pr.step = 0;
       if (SHARED && sees) pr = prefix_rows(p, ps, b, h);
       r = join_partials(
           (ns + pr.n - share + split - 1) / split, lane,
           [&](int k) {
             if (SHARED) k = share + k * split;
             if (SHARED && k >= ns)
-              return __ldcg(p.pre_lse + pr.row0 + static_cast<size_t>(k - ns) * 256);
+              return __ldcg(p.pre_lse + pr.row0 + (k - ns) * pr.step);
             return __ldcg(p.ws_lse + static_cast<size_t>(slots[k]) * p.Hq + h);
           },
           [&](int k) {
             if (SHARED) k = share + k * split;
             if (SHARED && k >= ns)
-              return __ldcg(po + (pr.row0 + static_cast<size_t>(k - ns) * 256) * (kDecD / 4) + lane);
+              return __ldcg(po + (pr.row0 + (k - ns) * pr.step) * (kDecD / 4) + lane);
             return __ldcg(wo + (static_cast<size_t>(slots[k]) * p.Hq + h) * (kDecD / 4) + lane);
           });
     }
@@ -1335,7 +1337,10 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   pre.work.pages = prefix_pages;
   pre.work.max_pages = max_prefix_pages;
   const long long pairs = (static_cast<long long>(B) * G + 255) / 256;
-  const long long items = pairs * Hkv;
+  pre.work.pair_groups = static_cast<int>((pairs + kPrefixTeam - 1) / kPrefixTeam);
+  pre.work.team =
+      static_cast<int>((pairs + pre.work.pair_groups - 1) / pre.work.pair_groups);
+  const long long items = static_cast<long long>(Hkv) * pre.work.pair_groups;
   const long long tiles =
       (static_cast<long long>(max_prefix_pages) * kPage + kPrefixTile - 1) / kPrefixTile;
   if (items * tiles > 0x7fffffffLL - nsm || static_cast<long long>(B) * Hq > 0x7fffffffLL - 256)
@@ -1352,10 +1357,10 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   // 32768 shared keys / 64 with 4096 at 2050 and 350 ns: 318 / 106, 700: 181 / 106, 1000:
   // 170 / 107, 1400: 178 / 126, 2000: 190 / 150, 3000: 219 / 199.
   pre.work.tile_ns = static_cast<long long>(B) * G > 128 ? 2050 : 1800;
-  pre.work.page_ns = 950;
+  pre.work.page_ns = 750;
   pre.work.ctas = nsm;
-  // segments write to slot CTA + item
-  const size_t pre_rows = pre.work.together ? static_cast<size_t>(nsm + items) * 256 : 0;
+  // segments write to slot (team + item) * team size + member
+  const size_t pre_rows = pre.work.together ? (nsm + items * pre.work.team) * size_t(256) : 0;
   const size_t pre_bytes = (pre_rows * (kDecD + 1) * sizeof(float) + 255) & ~size_t(255);
   cudaMemPool_t pool;
   int rc = get_pool(device, &pool);

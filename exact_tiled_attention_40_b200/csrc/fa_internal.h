@@ -141,6 +141,7 @@ int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device);
 
 // Shared-prefix attention: how its work is split (see prefix_split.cuh).
 constexpr int kPrefixTile = 128;        // keys per tile
+constexpr int kPrefixTeam = 8;          // CTAs of a team at most
 // Pages that a CTA streams at least: fewer make more partials than they save time (us with
 // 2 / 3 / 4: 2 sequences of 64 pages 17.0 / 15.5 / 16.0, 16 of 16 14.7 / 13.8 / 14.5).
 constexpr int kOwnMinPages = 3;
@@ -150,7 +151,9 @@ struct PrefixWork {
   int max_pages = 0;                    // bound on it
   bool together = true;                 // attended for the whole batch at once
   int pairs = 0;                        // 256-row pairs of a KV head's B * G rows
-  int items = 0;                        // Hkv * pairs
+  int team = 0;                         // pairs that as many CTAs take together
+  int pair_groups = 0;                  // ceil(pairs / team)
+  int items = 0;                        // Hkv * pair_groups
   int tile_ns = 0;                      // estimated time of a key tile of a pair on an SM
   int page_ns = 0;                      // of a streamed page
   int ctas = 0;                         // grid of the prefix and of the stream kernel

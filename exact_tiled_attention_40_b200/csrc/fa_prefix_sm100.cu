@@ -7,13 +7,14 @@
 // 4 * B * Hq * 128 flops against 4 * 128 * Hkv bytes, so a batch of a few dozen rows a
 // KV head is bound by HBM and one of a few hundred by the tensor cores.
 //
-// The work is a list of (KV head, pair of 128-row tiles, 128-key tile) units; of the C CTAs
-// that prefix_split.cuh gives it, CTA c takes the equal contiguous share
-// [c W / C, (c + 1) W / C) of its W units, whatever the prefix length, so that few rows over
-// a long prefix still use every SM.  A share that spans several (head, pair) items is cut
-// into segments; every segment writes its normalised partial output and LSE in fp32 to slot
-// c + item (unique: along the list c, item or both grow by one), and the decode merge joins
-// a row's segments with the partials of its own keys by their LSE.
+// The work is a list of (KV head, group of pairs of 128-row tiles, 128-key tile) units for
+// teams of CTAs, a pair each; of the C teams that prefix_split.cuh gives it, team c takes
+// the equal contiguous share [c W / C, (c + 1) W / C) of its W units, whatever the prefix
+// length, so that few rows over a long prefix still use every SM.  A share that spans
+// several (head, group) items is cut into segments; every segment writes its normalised
+// partial output and LSE in fp32 to a member's slot of c + item (unique: along the list c,
+// item or both grow by one), and the decode merge joins a row's segments with the partials
+// of its own keys by their LSE.
 //
 // Within a segment this is the online-softmax pipeline of the forward kernel on
 // tcgen05 (see there for the roles and the tensor-memory plan): a producer warp gathers
@@ -70,31 +71,37 @@ struct PrefixParams {
   uint64_t timeout_ns;
 };
 
-// A segment: key tiles [j0, j1) of rows [256 pair, 256 pair + 256) of KV head hkv.
+// A segment: key tiles [j0, j1) of rows [256 pair, 256 pair + 256) of KV head hkv, whose
+// partial results go to slot `slot`.
 struct Segment {
-  int item, hkv, pair, j0, j1;
+  int slot, hkv, pair, j0, j1;
   bool two;          // the pair's second row tile holds rows
 };
 struct SegmentWalker {
-  int u, u1, nt;
-  __device__ SegmentWalker(int cta, int C, const PrefixSplit& sp) {
+  int u, u1, nt, team, member;
+  __device__ SegmentWalker(int cta, const PrefixWork& w, const PrefixSplit& sp) {
     nt = sp.nt;
     u = u1 = 0;
-    if (cta < sp.ctas) {
-      u = share_edge(cta, sp.units, sp.ctas);
-      u1 = share_edge(cta + 1, sp.units, sp.ctas);
+    team = cta / w.team;
+    member = cta - team * w.team;
+    if (team < sp.teams) {
+      u = share_edge(team, sp.units, sp.teams);
+      u1 = share_edge(team + 1, sp.units, sp.teams);
     }
   }
   __device__ bool next(const PrefixParams& p, Segment& s) {
-    if (u >= u1) return false;
-    s.item = u / nt;
-    s.j0 = u - s.item * nt;
-    s.j1 = min(nt, s.j0 + (u1 - u));
-    s.hkv = s.item / p.w.pairs;
-    s.pair = s.item - s.hkv * p.w.pairs;
-    s.two = s.pair * 256 + kBM < p.B * p.G;
-    u += s.j1 - s.j0;
-    return true;
+    while (u < u1) {
+      const int item = u / nt;
+      s.slot = (team + item) * p.w.team + member;
+      s.j0 = u - item * nt;
+      s.j1 = min(nt, s.j0 + (u1 - u));
+      s.hkv = item / p.w.pair_groups;
+      s.pair = (item - s.hkv * p.w.pair_groups) * p.w.team + member;
+      s.two = s.pair * 256 + kBM < p.B * p.G;
+      u += s.j1 - s.j0;
+      if (s.pair < p.w.pairs) return true;       // else the last group has fewer pairs
+    }
+    return false;
   }
 };
 
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pg = lane / kChunks, ch = lane % kChunks;
       int pos = 0, segs = 0;
       bool ok = true;
-      SegmentWalker walk(cta, C, sp);
+      SegmentWalker walk(cta, p.w, sp);
       Segment s;
       while (ok && walk.next(p, s)) {
         if (segs > 0 && !wait_all(q_empty, (segs - 1) & 1)) break;
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int pos = 0, segs = 0;
       int tiles[2] = {0, 0};   // S tiles of each row tile in earlier segments (phases)
-      SegmentWalker walk(cta, C, sp);
+      SegmentWalker walk(cta, p.w, sp);
       Segment s;
       while (ok && walk.next(p, s)) {
         const int n = s.j1 - s.j0;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = smem + kStageOff + warp * kStageBytes;
     int tiles = 0, outs = 0;
     bool ok = true;
-    SegmentWalker walk(cta, C, sp);
+    SegmentWalker walk(cta, p.w, sp);
     Segment s;
     while (ok && walk.next(p, s)) {
       if (t == 1 && !s.two) continue;
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The warp's 32 rows, 32 columns at a time: through its staging box (16-byte chunk
       // k of row r at k ^ (r & 7)), so that 8 lanes write 128 contiguous bytes of a row.
       const float inv_l = l == 0.f ? 0.f : 1.f / l;   // 0: every score was -inf (then LSE is)
-      const size_t row0 = static_cast<size_t>(cta + s.item) * 256 + t * kBM + (warp & 3) * 32;
+      const size_t row0 = static_cast<size_t>(s.slot) * 256 + t * kBM + (warp & 3) * 32;
       const int rows = min(32, p.B * p.G - (s.pair * 256 + t * kBM + (warp & 3) * 32));
 #pragma unroll 1
       for (int c = 0; c < kD / 32; ++c) {

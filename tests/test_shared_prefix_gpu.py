@@ -108,49 +108,57 @@ def spread(seed, B, hi):
 @pytest.mark.parametrize("B,Hq,Hkv,P,hi", [
     (1, 1, 1, 1, 1), (1, 8, 2, 8, 40), (2, 8, 8, 9, 0), (5, 16, 2, 7, 33), (7, 8, 2, 65, 200),
     (33, 16, 16, 12, 50), (64, 32, 8, 16, 100), (65, 4, 1, 40, 20), (129, 4, 2, 3, 17),
-    (257, 8, 8, 5, 20), (40, 64, 8, 33, 30), (3, 10, 5, 130, 9), (300, 8, 1, 17, 3)])
+    (257, 8, 8, 5, 20), (40, 64, 8, 33, 30), (3, 10, 5, 130, 9), (300, 8, 1, 17, 3),
+    (70, 9, 9, 16, 40), (5, 22, 11, 220, 30), (600, 8, 1, 2, 5), (9, 32, 16, 120, 90),
+    (2, 8, 8, 520, 70)])
 def test_matches_the_oracle(cuda_device, B, Hq, Hkv, P, hi):
     s = make(B + P, B, Hq, Hkv, P, spread(P, B, hi), cuda_device)
     o, lse = fa.decode_shared_prefix(*on_device(s, cuda_device))
     check(o, lse, s)
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])       # streamed, direct
-def test_shorter_sequences_and_padding_rows(cuda_device, Hq, Hkv):
-    own = np.array([-400, -1, 0, 1, 15, 16, 17, -384, -16, -399, 250, -400])
-    s = make(3, 12, Hq, Hkv, 25, own, cuda_device)
+# a few copies of the shared keys are streamed with the own ones, many are attended at
+# once; 16 KV heads go through the stream kernel in two groups
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
+@pytest.mark.parametrize("P", [25, 90])
+def test_shorter_sequences_and_padding_rows(cuda_device, Hq, Hkv, P):
+    own = np.array([-16 * P, -1, 0, 1, 15, 16, 17, -384, -16, 1 - 16 * P, 250, -16 * P])
+    s = make(3, 12, Hq, Hkv, P, own, cuda_device)
     assert s["lens"].min() == 0
     check(*fa.decode_shared_prefix(*on_device(s, cuda_device)), s)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-def test_all_rows_empty(cuda_device, Hq, Hkv):
-    s = make(4, 5, Hq, Hkv, 4, [-64] * 5, cuda_device)
+@pytest.mark.parametrize("P", [4, 230])
+def test_all_rows_empty(cuda_device, Hq, Hkv, P):
+    s = make(4, 5, Hq, Hkv, P, [-16 * P] * 5, cuda_device)
     check(*fa.decode_shared_prefix(*on_device(s, cuda_device)), s)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
 def test_count_below_its_bound_and_none_shared(cuda_device, Hq, Hkv):
-    for P, bound in ((3, 50), (0, 50), (0, 0)):
+    for P, bound in ((3, 50), (0, 50), (0, 0), (3, 130), (0, 130)):
         s = make(5, 9, Hq, Hkv, P, spread(1, 9, 70), cuda_device, max_prefix=bound)
-        s["table"] = np.pad(s["table"], ((0, 0), (0, 60)))
+        s["table"] = np.pad(s["table"], ((0, 0), (0, 130)))
         check(*fa.decode_shared_prefix(*on_device(s, cuda_device)), s)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-def test_a_row_of_the_block_table_as_the_prefix(cuda_device, Hq, Hkv):
-    s = make(6, 6, Hq, Hkv, 10, spread(2, 6, 40), cuda_device)
+@pytest.mark.parametrize("P", [10, 190])
+def test_a_row_of_the_block_table_as_the_prefix(cuda_device, Hq, Hkv, P):
+    s = make(6, 6, Hq, Hkv, P, spread(2, 6, 40), cuda_device)
     q, kc, vc, _, lens, _, pages = on_device(s, cuda_device)
     table = i32(s["table"], cuda_device)
     check(*fa.decode_shared_prefix(q, kc, vc, table, lens, table[2], pages), s)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-def test_counts_and_ids_out_of_range(cuda_device, Hq, Hkv):
-    s = make(7, 6, Hq, Hkv, 10, spread(3, 6, 40), cuda_device)
+@pytest.mark.parametrize("P", [10, 190])
+def test_counts_and_ids_out_of_range(cuda_device, Hq, Hkv, P):
+    s = make(7, 6, Hq, Hkv, P, spread(3, 6, 40), cuda_device)
     q, kc, vc, _, lens, prefix, pages = on_device(s, cuda_device)
     table = i32(s["table"], cuda_device)
-    for bad in (-1, 11, 2 ** 31 - 1):             # counts as no shared page
+    for bad in (-1, P + 1, 2 ** 31 - 1):             # counts as no shared page
         o, lse = fa.decode_shared_prefix(q, kc, vc, table, lens, prefix,
                                          torch.full_like(pages, bad))
         assert fa.device_status() == 5
@@ -165,16 +173,17 @@ def test_counts_and_ids_out_of_range(cuda_device, Hq, Hkv):
         check(o, lse, z)
 
 
-def test_lowest_and_infinite_scores(cuda_device):
+@pytest.mark.parametrize("P", [20, 270])
+def test_lowest_and_infinite_scores(cuda_device, P):
     """Scores of -inf over the whole prefix: it takes no weight; large scores saturate."""
-    s = make(8, 4, 8, 2, 20, np.array([5, 0, 40, 1]), cuda_device, garbage=False)
+    s = make(8, 4, 8, 2, P, np.array([5, 0, 40, 1]), cuda_device, garbage=False)
     s["q"][:] = 0
     s["q"][..., 0] = 1
     at = torch.tensor(s["prefix"])
     s["kc"][at, :, :, 0] = float("-inf")
     q, kc, vc, table, lens, prefix, pages = on_device(s, cuda_device)
     o, lse = fa.decode_shared_prefix(q, kc, vc, table, lens, prefix, pages)
-    t = dict(s, lens=np.array([5, 0, 40, 1]), table=s["table"][:, 20:], P=0,
+    t = dict(s, lens=np.array([5, 0, 40, 1]), table=s["table"][:, P:], P=0,
              own=np.array([5, 0, 40, 1]))
     check(o, lse, t)
     s["kc"][at, :, :, 0] = 3e4                    # far above the own keys', one far above all
@@ -186,9 +195,10 @@ def test_lowest_and_infinite_scores(cuda_device):
     assert fa.device_status() == 0
 
 
-def test_equal_to_plain_decode_without_lse(cuda_device):
+@pytest.mark.parametrize("P", [50, 60])
+def test_equal_to_plain_decode_without_lse(cuda_device, P):
     """The same numbers as fa_decode_paged within both calls' roundings."""
-    s = make(9, 20, 32, 8, 50, spread(4, 20, 300), cuda_device)
+    s = make(9, 20, 32, 8, P, spread(4, 20, 300), cuda_device)
     q, kc, vc, _, lens, prefix, pages = on_device(s, cuda_device)
     table = i32(s["table"], cuda_device)
     o, none = fa.decode_shared_prefix(q, kc, vc, table, lens, prefix, pages, return_lse=False)
@@ -265,7 +275,7 @@ def test_graphs_streams_and_calls_at_once(cuda_device, Hq, Hkv):
     s = cases[0]
     short = dict(s, lens=s["lens"].copy(), own=s["own"].copy())
     short["own"] = np.minimum(short["own"], 16)
-    short["lens"] = 640 + short["own"]
+    short["lens"] = 640 + short["own"]           # (40 shared pages)
     ins[0][4].copy_(i32(short["lens"], dev))
     graphs[0].replay()
     check(*outs[0], short)
