@@ -170,7 +170,12 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
                          int device);
 
 // Raises a kernel's dynamic shared-memory limit, once per device and context.
-enum SmemKernel : int { kSmemExtend = 0, kSmemPrefix, kSmemKernels };
+enum SmemKernel : int {
+  kSmemExtend = 0,
+  kSmemExtendRows,
+  kSmemPrefix,
+  kSmemKernels
+};
 int raise_smem_limit(const void* kernel, int bytes, int device, SmemKernel which);
 
 // Release cached per-device resources owned by the decode path.

@@ -381,7 +381,7 @@ int fa_decode_shared_prefix(const void* q, const void* kcache, const void* vcach
  * tokens get slot -1) and a free_count outside [0, num_pages] (which counts as 0).
  * From the first sequence on whose pages or tokens do not fit free_count or
  * max_tokens, sequences stay as they are and FA_ERR_DEVICE_NO_PAGES is raised.
- * B <= 16384; page_size == 16.  One launch; nothing is allocated.
+ * B <= 16384; page_size == 16.  One launch or two; nothing is allocated.
  */
 int fa_extend_pages(int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
                     const int32_t* free_pages, const int32_t* free_count, int32_t* seq_lens_out,

@@ -55,7 +55,8 @@ def check(got, s, max_tokens):
 
 @pytest.mark.parametrize("B,hi,new_hi,new_lo", [
     (1, 0, 1, 1), (1, 40, 17, 0), (3, 40, 0, 0), (64, 500, 1, 1), (33, 60, 100, 0),
-    (1000, 70, 9, 0), (1025, 40, 3, 1), (2500, 0, 33, 0), (16384, 20, 2, 0)])
+    (1000, 70, 9, 0), (1025, 40, 3, 1), (2500, 0, 33, 0), (16384, 20, 2, 0),
+    (256, 90, 7, 0), (257, 90, 7, 0), (301, 300, 60, 1)])
 def test_extension_matches_the_oracle(cuda_device, B, hi, new_hi, new_lo):
     s = inputs(B + hi, B, hi, new_hi, -(-(hi + new_hi) // 16) + 1, spare=5, new_lo=new_lo)
     total = int(s["new"].sum())
