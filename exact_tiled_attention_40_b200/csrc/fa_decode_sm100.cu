@@ -87,9 +87,11 @@ constexpr int kStreamSmemBudget = 200 * 1024;
 constexpr int kDynDiv = 16;    // 1 / kDynDiv of each share is dynamic
 constexpr int kDynUnit = 8;    // half-pages per dynamic unit (at least)
 // SHARED: the CTAs that the shared-prefix kernel keeps waiting only take dynamic units, and
-// how long they wait is estimated, so more is dynamic (64 sequences of about 2050 own and
-// 4096 shared keys: 104.5 us, 106.9 with units of 2 pages).
-constexpr int dyn_div(bool shared) { return shared ? 8 : kDynDiv; }
+// how long they wait is estimated, so more is dynamic where most wait: a quarter (256
+// sequences of about 256 own and 32768 shared keys, where 124 of 148 wait: 168 us, 177 with
+// an eighth), else a 16th (64 of about 2050 own and 4096 shared, 11 wait: 102.8 us, with a
+// quarter 109.4).
+constexpr int kDynDivWait = 4;
 constexpr int dyn_unit(bool shared) { return shared ? 4 : kDynUnit; }
 constexpr int kMaxUnitsPerCta = 4;
 constexpr int kMaxStreamCtas = 204;                       // so a sequence has <= 1024 partials
@@ -416,15 +418,18 @@ __global__ void __launch_bounds__(1024) fa_decode_scan_kernel(const DecodeParams
 // C + B + u + b (unit u): along the list the sequence index and the share or
 // unit index never both stay the same, so the slots are distinct.
 struct StreamSplit {
-  int U, NUc;
+  int U, NUc, div;         // the last 1 / div of a share is dynamic
 };
+// (grid: CTAs with or without a share)
 template <bool SHARED>
-__device__ __forceinline__ StreamSplit stream_split(int H, int C, int cap) {
+__device__ __forceinline__ StreamSplit stream_split(int H, int C, int cap, int grid) {
   StreamSplit sp;
+  sp.div = SHARED && 2 * C < grid ? kDynDivWait : kDynDiv;
   sp.U = dyn_unit(SHARED);
   sp.NUc = 0;
-  const int per_cta = min(cap / C, kMaxUnitsPerCta);
-  const int dmax = ((H + C - 1) / C) / dyn_div(SHARED);
+  // (SHARED: cap is kMaxUnitsPerCta for every CTA of the grid, however many have shares)
+  const int per_cta = SHARED ? cap / C : min(cap / C, kMaxUnitsPerCta);
+  const int dmax = ((H + C - 1) / C) / sp.div;
   // (SHARED: a part of less than a unit would only add partials)
   if (per_cta > 0 && dmax >= (SHARED ? sp.U : 1)) {
     if ((dmax + sp.U - 1) / sp.U > per_cta) sp.U = (dmax + per_cta - 1) / per_cta;
@@ -435,12 +440,11 @@ __device__ __forceinline__ StreamSplit stream_split(int H, int C, int cap) {
 struct Share {
   int x0, y, x1;
 };
-template <bool SHARED>
 __device__ __forceinline__ Share share_of(int c, int H, int C, const StreamSplit& sp) {
   Share sh;
   sh.x0 = share_edge(c, H, C);
   sh.x1 = share_edge(c + 1, H, C);
-  sh.y = sh.x1 - (sp.NUc > 0 ? (sh.x1 - sh.x0) / dyn_div(SHARED) : 0);
+  sh.y = sh.x1 - (sp.NUc > 0 ? (sh.x1 - sh.x0) / sp.div : 0);
   return sh;
 }
 
@@ -502,9 +506,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (!p.pw.together) listed = shared_pages(p.pw);   // pages to be read by prefix_table
   }
   const int H = SHARED ? __ldcg(p.hb + p.B) : p.hb[p.B];
-  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap);
+  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap, gridDim.x);
   Share own = {0, 0, 0};
-  if (c < C) own = share_of<SHARED>(c, H, C, sp);
+  if (c < C) own = share_of(c, H, C, sp);
   __syncthreads();
 
   if (warp >= kConsumerWarps) {
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       if (lane == 0) u = atomicAdd(p.dyn_next, 1);
       u = __shfl_sync(0xffffffffu, u, 0);
       if (u >= n_units) break;
-      const Share sh = share_of<SHARED>(u / sp.NUc, H, C, sp);
+      const Share sh = share_of(u / sp.NUc, H, C, sp);
       const int xs = sh.y + (u % sp.NUc) * sp.U;
       if (xs < sh.x1) run_range(xs, min(sh.x1, xs + sp.U) - xs, C + p.B + u);
     }
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int xs = __ldcg(p.hb + b), xe = __ldcg(p.hb + b + 1);
-  PrefixSplit ps;
+  PrefixSplit ps = {};
   bool sees = false;                           // the sequence has the shared keys
   if constexpr (SHARED) {
     ps = prefix_split(p.pw, p.pw.ctas);
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
   }
   const int H = __ldcg(p.hb + p.B);
   const int C = SHARED ? ps.own_ctas : p.nctas;
-  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap);
+  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap, p.nctas);
   if (warp == 0) {
     int base = 0;
     // no own keys: an empty range
@@ -923,7 +927,7 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
       Share sh;
       int own = 0, k0 = 0, k1 = -1;
       if (cc <= c_last) {
-        sh = share_of<SHARED>(cc, H, C, sp);
+        sh = share_of(cc, H, C, sp);
         own = max(xs, sh.x0) < min(xe, sh.y) ? 1 : 0;
         const int lo = max(xs, sh.y), hi = min(xe, sh.x1);
         if (lo < hi) {
@@ -1126,7 +1130,7 @@ DecodePlan make_plan(int B, int Hq, int Hkv, int max_pages_per_seq, int nsm,
     // enough units for the dynamic part of every share of the longest possible list
     const long long h_max = 2LL * B * max_pages_per_seq;
     const long long per_cta =
-        ((h_max + pl.nctas - 1) / pl.nctas) / dyn_div(shared) / dyn_unit(shared) + 1;
+        ((h_max + pl.nctas - 1) / pl.nctas) / (shared ? kDynDivWait : kDynDiv) / dyn_unit(shared) + 1;
     pl.dyn_units_cap = static_cast<int>(std::min<long long>(per_cta * pl.nctas, 1 << 24));
   } else {
     pl.pps = direct_pps(B, max_pages_per_seq);
@@ -1355,9 +1359,10 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   // Measured on an SM: a key tile against two row tiles 1.9 to 2.3 us, against one 1.8 us;
   // a page of 8 KV heads 0.92 us.  What matters is their ratio.  us of 256 sequences with
   // 32768 shared keys / 64 with 4096 at 2050 and 350 ns: 318 / 106, 700: 181 / 106, 1000:
-  // 170 / 107, 1400: 178 / 126, 2000: 190 / 150, 3000: 219 / 199.
+  // 170 / 107, 1400: 178 / 126, 2000: 190 / 150, 3000: 219 / 199; in a long run at the power
+  // limit, where tiles take longer, 195 / 112 at 750 and 194 / 112 at 850.
   pre.work.tile_ns = static_cast<long long>(B) * G > 128 ? 2050 : 1800;
-  pre.work.page_ns = 750;
+  pre.work.page_ns = 850;
   pre.work.ctas = nsm;
   // segments write to slot (team + item) * team size + member
   const size_t pre_rows = pre.work.together ? (nsm + items * pre.work.team) * size_t(256) : 0;
