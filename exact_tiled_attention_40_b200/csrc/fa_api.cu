@@ -1,6 +1,6 @@
 // C-ABI entry points: argument validation on the host, error reporting and the
-// per-device error word.  Every compute step runs in the kernels of
-// fa_fwd_sm100.cu and fa_decode_sm100.cu; there is no host fallback.
+// per-device error word.  Every compute step runs in the kernels of the fa_*_sm100.cu
+// files beside this one; there is no host fallback.
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -952,6 +952,6 @@ void fa_release(void) {
   fa::g_cache_gen.fetch_add(1, std::memory_order_acq_rel);
 }
 
-int fa_version(void) { return 100; }
+int fa_version(void) { return 200; }
 
 }  // extern "C"
