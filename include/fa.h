@@ -469,7 +469,7 @@ int fa_qk_norm_rope_bwd_fp16(const void* q, const void* k, const void* dq_out, c
  *   q [T, Hq, D], k, v [T, Hkv, D] with q_stride, k_stride, v_stride elements between
  *       tokens; the other arguments as for fa_qk_norm_rope with B * N = T
  *   slot_map  [T] int64, as fa_extend_pages writes it.  A negative slot marks a padding
- *       row, of which nothing is read but the slot and nothing is written, q_out
+ *       row, of which nothing is used but the slot and nothing is written, q_out
  *       included; a slot beyond the pool raises FA_ERR_DEVICE_INDEX and is treated
  *       alike.  Slots must be distinct: one that is given twice holds a mixture.
  * The attention entry points read whole pages: fa_fwd_paged needs finite numbers in
