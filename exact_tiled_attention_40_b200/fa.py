@@ -116,15 +116,13 @@ def _stream(device):
 
 # Checks of the calls that a serving step makes once a layer: a few hundred nanoseconds
 # each counts there, so the texts are put together only for a refusal.
-def _on_current_device(where, *tensors):
+def _on_current_device(where, first, *tensors):
     """The kernels run on the current device: refuses tensors (None: absent) elsewhere."""
-    current = None
+    index = first.get_device()                  # -1: not on a CUDA device
+    if index < 0 or index != torch.cuda.current_device():
+        raise FAError(1, where, "tensors must live on the current CUDA device")
     for t in tensors:
-        if t is None:
-            continue
-        if current is None and t.is_cuda:
-            current = torch.cuda.current_device()
-        if not t.is_cuda or t.get_device() != current:
+        if t is not None and t.get_device() != index:
             raise FAError(1, where, "tensors must live on the current CUDA device")
 
 
@@ -136,14 +134,15 @@ def _dtypes(where, dtype, *tensors):
 
 
 def _shape(where, name, t, *want):
-    if t.shape != want:
+    if t is not None and t.shape != want:
         raise FAError(1, where, f"{name} must have shape {list(want)}, not {list(t.shape)}")
 
 
 def _dims(where, name, t, n):
-    if t.dim() != n:
-        raise FAError(1, where, f"{name} must have {n} dimensions, not {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise FAError(1, where, f"{name} must have {n} dimensions, not {len(shape)}")
+    return shape
 
 
 _STRIDES = {1: lambda a: (1,), 2: lambda a, b: (b, 1), 3: lambda a, b, c: (b * c, c, 1),
@@ -485,14 +484,16 @@ def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
     _dtypes(where, torch.bfloat16, q, kcache, vcache)
     _dtypes(where, torch.int32, block_table, seq_lens, prefix_table, prefix_pages)
     B, Hq, D = _dims(where, "q", q, 3)
-    num_pages, page_size, Hkv, _ = cache = _dims(where, "kcache", kcache, 4)
-    _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
-    _shape(where, "vcache", vcache, *cache)
-    _, max_pages = _dims(where, "block_table", block_table, 2)
-    _shape(where, "block_table", block_table, B, max_pages)
-    _shape(where, "seq_lens", seq_lens, B)
+    num_pages, page_size, Hkv, width = cache = _dims(where, "kcache", kcache, 4)
+    rows, max_pages = _dims(where, "block_table", block_table, 2)
     max_prefix, = _dims(where, "prefix_table", prefix_table, 1)
-    _shape(where, "prefix_pages", prefix_pages, 1)
+    if (width != D or vcache.shape != cache or rows != B or seq_lens.shape != (B,)
+            or prefix_pages.shape != (1,)):
+        _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
+        _shape(where, "vcache", vcache, *cache)
+        _shape(where, "block_table", block_table, B, max_pages)
+        _shape(where, "seq_lens", seq_lens, B)
+        _shape(where, "prefix_pages", prefix_pages, 1)
     if scale is None:
         scale = D ** -0.5
     q = q.contiguous()
@@ -527,10 +528,12 @@ def extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, num_pa
     _on_current_device(where, block_table, seq_lens, new_lens, free_pages, free_count)
     _dtypes(where, torch.int32, block_table, seq_lens, new_lens, free_pages, free_count)
     B, max_pages = _dims(where, "block_table", block_table, 2)
-    _shape(where, "seq_lens", seq_lens, B)
-    _shape(where, "new_lens", new_lens, B)
-    _shape(where, "free_pages", free_pages, num_pages)
-    _shape(where, "free_count", free_count, 1)
+    if (seq_lens.shape != (B,) or new_lens.shape != (B,) or free_pages.shape != (num_pages,)
+            or free_count.shape != (1,)):
+        _shape(where, "seq_lens", seq_lens, B)
+        _shape(where, "new_lens", new_lens, B)
+        _shape(where, "free_pages", free_pages, num_pages)
+        _shape(where, "free_count", free_count, 1)
     if not block_table.is_contiguous():
         raise FAError(1, where, "block_table is written in place and must be contiguous")
     if max_tokens < 0:
@@ -573,21 +576,20 @@ def _norm_rope_args(where, q, k, q_weight, k_weight, table, positions, pair_axis
     _dtypes(where, dtype, k, q_weight, k_weight)
     _dtypes(where, torch.float32, table)
     _dtypes(where, torch.int32, positions)
-    sizes = _dims(where, "q", q, lead + 2)
-    D = sizes[-1]
-    _shape(where, "k", k, *sizes[:lead], _dims(where, "k", k, lead + 2)[lead], D)
-    if q_weight is not None:
-        _shape(where, "q_weight", q_weight, D)
-    if k_weight is not None:
-        _shape(where, "k_weight", k_weight, D)
+    sizes, k_sizes = _dims(where, "q", q, lead + 2), _dims(where, "k", k, lead + 2)
     max_pos, rot = _dims(where, "table", table, 2)
+    D = sizes[-1]
     tokens = sizes[0] if lead == 1 else sizes[0] * sizes[1]
-    if positions.dim() == 1:
-        _shape(where, "positions", positions, tokens)
-        axes = 1
-    else:
-        axes = _dims(where, "positions", positions, 2)[0]
-        _shape(where, "positions", positions, axes, tokens)
+    at = positions.shape
+    axes = 1 if len(at) == 1 else at[0]
+    if (k_sizes[0] != sizes[0] or k_sizes[lead - 1] != sizes[lead - 1] or k_sizes[-1] != D
+            or (q_weight is not None and q_weight.shape != (D,))
+            or (k_weight is not None and k_weight.shape != (D,))
+            or (at != (tokens,) and at != (axes, tokens))):
+        _shape(where, "k", k, *sizes[:lead], k_sizes[lead], D)
+        _shape(where, "q_weight", q_weight, D)
+        _shape(where, "k_weight", k_weight, D)
+        _shape(where, "positions", positions, *_dims(where, "positions", positions, 2)[:1], tokens)
     if axes != 1:
         if pair_axis is None:
             raise FAError(1, where, "pair_axis is needed with more than one axis")
@@ -710,10 +712,11 @@ def append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table, p
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     _shape(where, "v", v, T, Hkv, D)
-    num_pages, page_size, _, _ = cache = _dims(where, "kcache", kcache, 4)
-    _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
-    _shape(where, "vcache", vcache, *cache)
-    _shape(where, "slot_map", slot_map, T)
+    num_pages, page_size, heads, width = cache = _dims(where, "kcache", kcache, 4)
+    if heads != Hkv or width != D or vcache.shape != cache or slot_map.shape != (T,):
+        _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
+        _shape(where, "vcache", vcache, *cache)
+        _shape(where, "slot_map", slot_map, T)
     if not (kcache.is_contiguous() and vcache.is_contiguous()):
         raise FAError(1, where, "the caches are written in place and must be contiguous")
     q, q_stride = _head_rows(q)
