@@ -110,7 +110,7 @@ def spread(seed, B, hi):
     (33, 16, 16, 12, 50), (64, 32, 8, 16, 100), (65, 4, 1, 40, 20), (129, 4, 2, 3, 17),
     (257, 8, 8, 5, 20), (40, 64, 8, 33, 30), (3, 10, 5, 130, 9), (300, 8, 1, 17, 3),
     (70, 9, 9, 16, 40), (5, 22, 11, 220, 30), (600, 8, 1, 2, 5), (9, 32, 16, 120, 90),
-    (2, 8, 8, 520, 70)])
+    (2, 8, 8, 520, 70), (4200, 4, 1, 1, 20), (2, 8, 1, 600, 30000), (3, 64, 64, 50, 40)])
 def test_matches_the_oracle(cuda_device, B, Hq, Hkv, P, hi):
     s = make(B + P, B, Hq, Hkv, P, spread(P, B, hi), cuda_device)
     o, lse = fa.decode_shared_prefix(*on_device(s, cuda_device))

@@ -227,3 +227,36 @@ def test_many_calls_of_all_kinds_on_two_streams(cuda_device):
             for a, b in zip(alone, r):
                 assert torch.equal(a, b)
     assert fa.device_status() == 0
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """270,000 tokens of 64 heads of 128: 2.2e9 elements a tensor.  Rows at the start, in the
+    middle and at the end are what a call on those tokens alone gives, in both layouts."""
+    dev = cuda_device
+    T, H, D = 270000, 64, 128
+    gen = torch.Generator(device=dev).manual_seed(7)
+    x = torch.empty(1, T, H, D, dtype=torch.bfloat16, device=dev)
+    dy = torch.empty(1, H, T, D, dtype=torch.bfloat16, device=dev)
+    spots = [slice(0, 40), slice(131060, 131100), slice(T - 40, T)]
+    x.fill_(0.5)
+    dy.fill_(0.25)
+    for at in spots:
+        x[:, at] = torch.randn(1, 40, H, D, generator=gen, device=dev).bfloat16()
+        dy[:, :, at] = torch.randn(1, H, 40, D, generator=gen, device=dev).bfloat16()
+    none = torch.empty(1, T, 0, D, dtype=torch.bfloat16, device=dev)
+    few = torch.empty(1, 40, 0, D, dtype=torch.bfloat16, device=dev)
+    w = torch.randn(D, generator=gen, device=dev).bfloat16()
+    tab = torch.rand(64, D, generator=gen, device=dev)
+    pos = torch.arange(T, device=dev).remainder(64).int()
+    for first in (True, False):
+        y, _ = fa.qk_norm_rope(x, none, w, None, tab, pos, heads_first=first)
+        for at in spots:
+            z, _ = fa.qk_norm_rope(x[:, at], few, w, None, tab, pos[at], heads_first=first)
+            assert torch.equal(y[:, :, at] if first else y[:, at], z)
+        del y
+    dx, _, _, _ = fa.qk_norm_rope_backward(x, none, dy, none.transpose(1, 2), w, None, tab, pos)
+    for at in spots:
+        dz, _, _, _ = fa.qk_norm_rope_backward(x[:, at], few, dy[:, :, at], few.transpose(1, 2), w,
+                                               None, tab, pos[at])
+        assert torch.equal(dx[:, at], dz)
+    assert fa.device_status() == 0
