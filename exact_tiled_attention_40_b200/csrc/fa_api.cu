@@ -952,6 +952,6 @@ void fa_release(void) {
   fa::g_cache_gen.fetch_add(1, std::memory_order_acq_rel);
 }
 
-int fa_version(void) { return 200; }
+int fa_version(void) { return 100; }
 
 }  // extern "C"
