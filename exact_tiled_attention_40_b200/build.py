@@ -3,7 +3,8 @@
 Usage: ``python -m exact_tiled_attention_40_b200.build`` (or ``build()`` from
 Python).  Every .cu file under csrc/ is compiled with nvcc for sm_100a only and
 linked with the static CUDA runtime; the driver API is reached at run time
-through cudaGetDriverEntryPoint, so loading the library needs no GPU.
+through cudaGetDriverEntryPoint, so loading the library needs no GPU.  The
+compiled part of the Python binding, ``_step.so``, is built with g++ beside it.
 
 ``build(debug=True)`` (``--debug``) builds the same library with FA_DEBUG=1 into
 _build/debug/libfa_sm100.so: every tensor-memory load, store and wait first
@@ -18,12 +19,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa_sm100.so")
+BINDING = os.path.join(HERE, "_step.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libfa_sm100.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -64,12 +67,34 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
     return obj
 
 
+def _build_binding() -> str:
+    """The Python module of csrc/py_step.cpp (it calls the library by address)."""
+    src = os.path.join(CSRC, "py_step.cpp")
+    if _stale(BINDING, [src, os.path.join(ROOT, "include", "fa.h")]):
+        import torch
+        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+        paths = [inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               "-I", os.path.join(ROOT, "include"), *[f for p in paths for f in ("-isystem", p)],
+               src, "-o", BINDING, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+               "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return BINDING
+
+
 def build(verbose_ptxas: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
     os.makedirs(DEBUG_BUILD if debug else BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=len(sources)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, debug), sources))
+    binding.result()
     if _stale(lib, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", lib, *objs, "-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)

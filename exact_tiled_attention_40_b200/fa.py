@@ -1,7 +1,9 @@
 """Thin Python binding of the C ABI in include/fa.h (argument marshalling only).
 
 Every function forwards device pointers, sizes and the current CUDA stream to
-``libfa_sm100.so``; all arithmetic runs in that library's sm_100a kernels.
+``libfa_sm100.so``; all arithmetic runs in that library's sm_100a kernels.  The
+operators that a serving or training step calls once a layer go through a compiled
+binding (csrc/py_step.cpp), the others and the raw calls through ctypes.
 There is no fallback: if the library or a CUDA device is missing, calls raise.
 PyTorch is used for device memory and streams only.
 """
@@ -114,53 +116,24 @@ def _stream(device):
     return _raw_stream(index)
 
 
-# Checks of the calls that a serving step makes once a layer: a few hundred nanoseconds
-# each counts there, so the texts are put together only for a refusal.
-def _on_current_device(where, first, *tensors):
-    """The kernels run on the current device: refuses tensors (None: absent) elsewhere."""
-    index = first.get_device()                  # -1: not on a CUDA device
-    if index < 0 or index != torch.cuda.current_device():
-        raise FAError(1, where, "tensors must live on the current CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise FAError(1, where, "tensors must live on the current CUDA device")
+_step = None
 
 
-def _dtypes(where, dtype, *tensors):
-    for t in tensors:
-        if t is not None and t.dtype is not dtype:
-            raise FAError(1, where, f"a tensor of shape {list(t.shape)} must be {str(dtype)[6:]}, "
-                          f"not {str(t.dtype)[6:]}")
-
-
-def _shape(where, name, t, *want):
-    if t is not None and t.shape != want:
-        raise FAError(1, where, f"{name} must have shape {list(want)}, not {list(t.shape)}")
-
-
-def _dims(where, name, t, n):
-    shape = t.shape
-    if len(shape) != n:
-        raise FAError(1, where, f"{name} must have {n} dimensions, not {len(shape)}")
-    return shape
-
-
-_STRIDES = {1: lambda a: (1,), 2: lambda a, b: (b, 1), 3: lambda a, b, c: (b * c, c, 1),
-            4: lambda a, b, c, d: (b * c * d, c * d, d, 1)}
-
-
-def _new(like, dtype, *shape):
-    """An uninitialised contiguous tensor (empty_strided: half the cost of torch.empty)."""
-    return torch.empty_strided(shape, _STRIDES[len(shape)](*shape), dtype=dtype,
-                               device=like.device)
-
-
-def _aligned16(t):
-    """t (or None) contiguous and at a 16-byte boundary, copied where it is not."""
-    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
-        return t
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+def _native():
+    """The compiled binding of the step operators (csrc/py_step.cpp), calling the entry
+    points of the library that lib() has loaded."""
+    global _step
+    if _step is None:
+        try:
+            from . import _step as module
+        except ImportError as e:
+            raise FAError(-1, "load", f"the compiled binding is missing or does not load ({e}); run "
+                          "`python -m exact_tiled_attention_40_b200.build`")
+        l = lib()
+        module.bind({name: ctypes.cast(getattr(l, name), ctypes.c_void_p).value
+                     for name in _SIGS}, FAError)
+        _step = module
+    return _step
 
 
 def fa_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, causal, stream=None):
@@ -479,31 +452,8 @@ def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
     prefix_pages[0] (int32, on the device) entries of prefix_table [max_prefix_pages]
     (a row of block_table will do).  Sequences shorter than the shared pages take no
     part and are read through their own block_table row."""
-    where = "decode_shared_prefix"
-    _on_current_device(where, q, kcache, vcache, block_table, seq_lens, prefix_table, prefix_pages)
-    _dtypes(where, torch.bfloat16, q, kcache, vcache)
-    _dtypes(where, torch.int32, block_table, seq_lens, prefix_table, prefix_pages)
-    B, Hq, D = _dims(where, "q", q, 3)
-    num_pages, page_size, Hkv, width = cache = _dims(where, "kcache", kcache, 4)
-    rows, max_pages = _dims(where, "block_table", block_table, 2)
-    max_prefix, = _dims(where, "prefix_table", prefix_table, 1)
-    if (width != D or vcache.shape != cache or rows != B or seq_lens.shape != (B,)
-            or prefix_pages.shape != (1,)):
-        _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
-        _shape(where, "vcache", vcache, *cache)
-        _shape(where, "block_table", block_table, B, max_pages)
-        _shape(where, "seq_lens", seq_lens, B)
-        _shape(where, "prefix_pages", prefix_pages, 1)
-    if scale is None:
-        scale = D ** -0.5
-    q = q.contiguous()
-    o = torch.empty_like(q)
-    lse = _new(q, torch.float32, B, Hq) if return_lse else None
-    fa_decode_shared_prefix(q, kcache.contiguous(), vcache.contiguous(),
-                            block_table.contiguous(), seq_lens.contiguous(),
-                            prefix_table.contiguous(), prefix_pages, o, B, Hq, Hkv, D, page_size,
-                            scale, max_pages, max_prefix, num_pages, lse)
-    return o, lse
+    return _native().decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
+                                          prefix_pages, scale, return_lse)
 
 
 def fa_extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, seq_lens_out,
@@ -524,80 +474,8 @@ def extend_pages(block_table, seq_lens, new_lens, free_pages, free_count, num_pa
     of the first free_count[0] entries of free_pages [num_pages].  Returns (seq_lens +
     new_lens [B], cu_seqlens_q [B+1], positions [max_tokens] int32, slot_map [max_tokens]
     int64, pages left [1])."""
-    where = "extend_pages"
-    _on_current_device(where, block_table, seq_lens, new_lens, free_pages, free_count)
-    _dtypes(where, torch.int32, block_table, seq_lens, new_lens, free_pages, free_count)
-    B, max_pages = _dims(where, "block_table", block_table, 2)
-    if (seq_lens.shape != (B,) or new_lens.shape != (B,) or free_pages.shape != (num_pages,)
-            or free_count.shape != (1,)):
-        _shape(where, "seq_lens", seq_lens, B)
-        _shape(where, "new_lens", new_lens, B)
-        _shape(where, "free_pages", free_pages, num_pages)
-        _shape(where, "free_count", free_count, 1)
-    if not block_table.is_contiguous():
-        raise FAError(1, where, "block_table is written in place and must be contiguous")
-    if max_tokens < 0:
-        raise FAError(1, where, "max_tokens must not be negative")
-    lens_out, cu, left, positions = _new(block_table, torch.int32, 2 * B + 2 + max_tokens).split(
-        (B, B + 1, 1, max_tokens))
-    slots = _new(block_table, torch.int64, max_tokens)
-    fa_extend_pages(block_table, seq_lens.contiguous(), new_lens.contiguous(),
-                    free_pages.contiguous(), free_count, lens_out, left, cu, positions, slots, B,
-                    max_pages, num_pages, 16, max_tokens)
-    return lens_out, cu, positions, slots, left
-
-
-def _head_rows(t):
-    """t [..., H, D] as the library reads token-major rows: t itself where each token's
-    heads are contiguous and one stride leads from token to token (a view of a QKV
-    projection), a contiguous copy otherwise; and that stride in elements."""
-    *lead, H, D = t.shape
-    *steps, across, inner = t.stride()
-    stride, span = H * D, 1                     # no step from token to token: any will do
-    for i in range(len(lead) - 1, -1, -1):
-        if lead[i] != 1:
-            if span == 1:
-                stride = steps[i]
-            elif steps[i] != stride * span:
-                return _aligned16(t.contiguous()), H * D
-            span *= lead[i]
-    if (inner == 1 and (across == D or H == 1) and stride >= H * D and stride % 8 == 0
-            and span and t.data_ptr() % 16 == 0):
-        return t, stride
-    return _aligned16(t.contiguous()), H * D
-
-
-def _norm_rope_args(where, q, k, q_weight, k_weight, table, positions, pair_axis, lead):
-    """Checks shared by the norm + rotation calls; contiguous weights, table, positions and
-    axes, and the sizes of the table."""
-    dtype = q.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise FAError(1, where, "q must be bf16 or fp16")
-    _dtypes(where, dtype, k, q_weight, k_weight)
-    _dtypes(where, torch.float32, table)
-    _dtypes(where, torch.int32, positions)
-    sizes, k_sizes = _dims(where, "q", q, lead + 2), _dims(where, "k", k, lead + 2)
-    max_pos, rot = _dims(where, "table", table, 2)
-    D = sizes[-1]
-    tokens = sizes[0] if lead == 1 else sizes[0] * sizes[1]
-    at = positions.shape
-    axes = 1 if len(at) == 1 else at[0]
-    if (k_sizes[0] != sizes[0] or k_sizes[lead - 1] != sizes[lead - 1] or k_sizes[-1] != D
-            or (q_weight is not None and q_weight.shape != (D,))
-            or (k_weight is not None and k_weight.shape != (D,))
-            or (at != (tokens,) and at != (axes, tokens))):
-        _shape(where, "k", k, *sizes[:lead], k_sizes[lead], D)
-        _shape(where, "q_weight", q_weight, D)
-        _shape(where, "k_weight", k_weight, D)
-        _shape(where, "positions", positions, *_dims(where, "positions", positions, 2)[:1], tokens)
-    if axes != 1:
-        if pair_axis is None:
-            raise FAError(1, where, "pair_axis is needed with more than one axis")
-        _dtypes(where, torch.uint8, pair_axis)
-        _shape(where, "pair_axis", pair_axis, rot // 2)
-        pair_axis = pair_axis.contiguous()
-    return (_aligned16(q_weight), _aligned16(k_weight), _aligned16(table), positions.contiguous(),
-            pair_axis, rot, max_pos, axes)
+    return _native().extend_pages(block_table, seq_lens, new_lens, free_pages, free_count,
+                                  num_pages, max_tokens)
 
 
 def fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N, Hq,
@@ -619,21 +497,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis=None, eps
     table [max_positions, rot_dim] fp32 (cosines, then sines) at positions
     [n_axes, B * N] (or [B * N]) int32, pair j along axis pair_axis[j] (uint8).
     Returns q and k as [B, H, N, D] (heads_first, what `attention` takes) or [B, N, H, D]."""
-    where = "qk_norm_rope"
-    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis)
-    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
-        where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
-    B, N, Hq, D = q.shape
-    Hkv = k.shape[2]
-    q, q_stride = _head_rows(q)
-    k, k_stride = _head_rows(k)
-    if heads_first:
-        q_out, k_out = _new(q, q.dtype, B, Hq, N, D), _new(q, q.dtype, B, Hkv, N, D)
-    else:
-        q_out, k_out = _new(q, q.dtype, B, N, Hq, D), _new(q, q.dtype, B, N, Hkv, D)
-    fa_qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, q_out, k_out, B, N, Hq,
-                    Hkv, D, q_stride, k_stride, rot, max_pos, axes, interleaved, heads_first, eps)
-    return q_out, k_out
+    return _native().qk_norm_rope(q, k, q_weight, k_weight, table, positions, pair_axis, eps,
+                                  interleaved, heads_first)
 
 
 def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, table, positions, pair_axis, dq,
@@ -655,32 +520,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table, posit
     """(dq, dk, dq_weight, dk_weight) of qk_norm_rope for the gradients dq_out, dk_out of its
     outputs: dq [B, N, Hq, D] and dk [B, N, Hkv, D] in q's dtype, the weights' in fp32
     (None where the weight is None)."""
-    where = "qk_norm_rope_backward"
-    _on_current_device(where, q, k, q_weight, k_weight, table, positions, pair_axis, dq_out, dk_out)
-    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
-        where, q, k, q_weight, k_weight, table, positions, pair_axis, 2)
-    _dtypes(where, q.dtype, dq_out, dk_out)
-    B, N, Hq, D = q.shape
-    Hkv = k.shape[2]
-    if heads_first:
-        _shape(where, "dq_out", dq_out, B, Hq, N, D)
-        _shape(where, "dk_out", dk_out, B, Hkv, N, D)
-    else:
-        _shape(where, "dq_out", dq_out, B, N, Hq, D)
-        _shape(where, "dk_out", dk_out, B, N, Hkv, D)
-    q, q_stride = _head_rows(q)
-    k, k_stride = _head_rows(k)
-    dq, dk = _new(q, q.dtype, B, N, Hq, D), _new(q, q.dtype, B, N, Hkv, D)
-    dwq = None if q_weight is None else _new(q, torch.float32, D)
-    dwk = None if k_weight is None else _new(q, torch.float32, D)
-    scratch = None
-    if q_weight is not None or k_weight is not None:
-        scratch = _new(q, torch.float32, 2 * QK_NORM_ROPE_SCRATCH_ROWS * D)
-    fa_qk_norm_rope_bwd(q, k, _aligned16(dq_out), _aligned16(dk_out), q_weight, k_weight, table,
-                        positions, pair_axis, dq, dk, dwq, dwk, scratch, B, N, Hq, Hkv, D, q_stride,
-                        k_stride, Hq * D, Hkv * D, rot, max_pos, axes, interleaved, heads_first,
-                        eps)
-    return dq, dk, dwq, dwk
+    return _native().qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table,
+                                           positions, pair_axis, eps, interleaved, heads_first)
 
 
 def fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis, slot_map, q_out,
@@ -702,32 +543,8 @@ def append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table, p
     pool kcache, vcache [num_pages, 16, Hkv, D], where K (normed and rotated) and V are written
     in place.  Returns q [T, Hq, D] for prefill_paged and the decode calls; rows of padding
     tokens are left unset."""
-    where = "append_paged"
-    _on_current_device(where, q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table,
-                       positions, pair_axis)
-    _dtypes(where, torch.bfloat16, q, v, kcache, vcache)
-    _dtypes(where, torch.int64, slot_map)
-    q_weight, k_weight, table, positions, pair_axis, rot, max_pos, axes = _norm_rope_args(
-        where, q, k, q_weight, k_weight, table, positions, pair_axis, 1)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    _shape(where, "v", v, T, Hkv, D)
-    num_pages, page_size, heads, width = cache = _dims(where, "kcache", kcache, 4)
-    if heads != Hkv or width != D or vcache.shape != cache or slot_map.shape != (T,):
-        _shape(where, "kcache", kcache, num_pages, page_size, Hkv, D)
-        _shape(where, "vcache", vcache, *cache)
-        _shape(where, "slot_map", slot_map, T)
-    if not (kcache.is_contiguous() and vcache.is_contiguous()):
-        raise FAError(1, where, "the caches are written in place and must be contiguous")
-    q, q_stride = _head_rows(q)
-    k, k_stride = _head_rows(k)
-    v, v_stride = _head_rows(v)
-    q_out = _new(q, q.dtype, T, Hq, D)
-    fa_append_paged(q, k, v, q_weight, k_weight, table, positions, pair_axis,
-                    slot_map.contiguous(), q_out, kcache, vcache, T, Hq, Hkv, D, page_size,
-                    num_pages, q_stride, k_stride, v_stride, rot, max_pos, axes, interleaved,
-                    eps)
-    return q_out
+    return _native().append_paged(q, k, v, kcache, vcache, slot_map, q_weight, k_weight, table,
+                                  positions, pair_axis, eps, interleaved)
 
 
 def device_status() -> int:

@@ -260,3 +260,49 @@ def test_offsets_past_32_bits(cuda_device):
                                                None, tab, pos[at])
         assert torch.equal(dx[:, at], dz)
     assert fa.device_status() == 0
+
+
+def test_the_binding_refuses_other_types_and_shapes(cuda_device):
+    dev = cuda_device
+    bf, i32 = torch.bfloat16, torch.int32
+
+    def z(*shape, dtype=bf):
+        return torch.zeros(*shape, dtype=dtype, device=dev)
+
+    q, k, w, tab, pos = z(2, 3, 4, 64), z(2, 3, 2, 64), z(64), z(9, 64, dtype=torch.float32), z(
+        6, dtype=i32)
+    kc = z(5, 16, 2, 64)
+    slots = z(3, dtype=torch.int64)
+    d = z(2, 8, 128)
+    pool = z(7, 16, 2, 128)
+    table, lens, pages = z(2, 4, dtype=i32), z(2, dtype=i32), z(1, dtype=i32)
+    rope = [q, k, w, w, tab, pos]
+    bwd = [q, k, z(2, 4, 3, 64), z(2, 2, 3, 64), w, w, tab, pos]
+    app = [q[0], k[0], k[0], kc, kc.clone(), slots, w, w, tab, pos[:3]]
+    ext = [table, lens, lens, z(7, dtype=i32), pages, 7, 5]
+    dec = [d, pool, pool, table, lens, table[0], pages]
+    for fn, args, changes in (
+            (fa.qk_norm_rope, rope, [(0, q.float()), (0, q[0]), (1, k.half()), (1, k[:1]),
+                                     (1, z(2, 3, 2, 128)), (2, z(65)), (3, w.half()), (4, w),
+                                     (4, tab.to(bf)), (5, pos.long()), (5, pos[:5]),
+                                     (5, z(2, 6, dtype=i32)), (0, q.cpu()), (4, tab.cpu())]),
+            (fa.qk_norm_rope_backward, bwd, [(2, z(2, 3, 4, 64)), (3, z(2, 2, 3, 64).half()),
+                                             (2, z(2, 4, 3, 64).cpu()), (4, z(32))]),
+            (fa.append_paged, app, [(0, q[0].half()), (2, z(3, 1, 64)), (3, z(5, 16, 1, 64)),
+                                    (3, kc.transpose(0, 1)), (4, z(4, 16, 2, 64)), (5, slots.int()),
+                                    (5, slots[:2]), (3, kc[:, ::2])]),
+            (fa.extend_pages, ext, [(0, table.long()), (0, lens), (0, table.t()), (1, lens[:1]),
+                                    (2, lens.long()), (3, z(6, dtype=i32)), (4, lens), (6, -1),
+                                    (1, lens.cpu())]),
+            (fa.decode_shared_prefix, dec, [(0, d.half()), (0, d[0]), (1, z(7, 16, 2, 64)),
+                                            (2, pool[:6]), (3, table[:1]), (4, lens.long()),
+                                            (5, table), (6, lens), (5, z(5, dtype=i32))])):
+        for at, wrong in changes:
+            bad = list(args)
+            bad[at] = wrong
+            with pytest.raises(fa.FAError):
+                fn(*bad)
+        fn(*args)                                    # and takes what is right
+    with pytest.raises(fa.FAError, match="pair_axis"):
+        fa.qk_norm_rope(q, k, w, w, tab, z(2, 6, dtype=i32))
+    assert fa.device_status() == 0
