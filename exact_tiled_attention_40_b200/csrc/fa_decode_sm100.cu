@@ -1488,6 +1488,36 @@ int check_decode_noalloc(int B, int Hq, int Hkv, int max_pages_per_seq, int nsm)
   return plan_noalloc(B, Hq, Hkv, max_pages_per_seq, nsm, &pl);
 }
 
+// Kernels are loaded at their first launch otherwise, and loading one may take device
+// memory: the first call on a device loads all that any later one can need.
+static int load_noalloc_kernels(int device) {
+  static int gen[64] = {};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> g(mu);
+  if (device < 0 || device >= 64) return set_error(FA_ERR_CUDA, "device ordinal out of range");
+  if (gen[device] == cache_generation()) return FA_OK;
+  const void* const kernels[] = {
+      reinterpret_cast<const void*>(fa_decode_scan_kernel<false>),
+      reinterpret_cast<const void*>(fa_decode_stream_kernel<1, false>),
+      reinterpret_cast<const void*>(fa_decode_stream_kernel<2, false>),
+      reinterpret_cast<const void*>(fa_decode_stream_kernel<4, false>),
+      reinterpret_cast<const void*>(fa_decode_stream_kernel<8, false>),
+      reinterpret_cast<const void*>(fa_decode_stream_merge_kernel<false>),
+      reinterpret_cast<const void*>(fa_decode_split_kernel<1>),
+      reinterpret_cast<const void*>(fa_decode_split_kernel<2>),
+      reinterpret_cast<const void*>(fa_decode_split_kernel<4>),
+      reinterpret_cast<const void*>(fa_decode_split_kernel<8>),
+      reinterpret_cast<const void*>(fa_decode_combine_kernel)};
+  for (const void* k : kernels) {
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, k);
+    if (e != cudaSuccess)
+      return set_error(FA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+  }
+  gen[device] = cache_generation();
+  return FA_OK;
+}
+
 int launch_decode_noalloc(const void* q, const void* kcache, const void* vcache,
                           const int32_t* block_table, const int32_t* seq_lens, void* o, float* lse,
                           int B, int Hq, int Hkv, int max_pages_per_seq, int num_pages,
@@ -1500,6 +1530,7 @@ int launch_decode_noalloc(const void* q, const void* kcache, const void* vcache,
   if (rc != FA_OK) return rc;
   float* scratch = nullptr;
   if ((rc = scratch_address(device, &scratch)) != FA_OK) return rc;
+  if ((rc = load_noalloc_kernels(device)) != FA_OK) return rc;
   return run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv,
                     max_pages_per_seq, num_pages, scale, pl, scratch, stream, device);
 }
