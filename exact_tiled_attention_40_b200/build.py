@@ -80,7 +80,7 @@ def _build_binding() -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                "-I", os.path.join(ROOT, "include"), *[f for p in paths for f in ("-isystem", p)],
                src, "-o", BINDING, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
-               "-ltorch_python"]
+               "-ltorch_cuda", "-ltorch_python"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -3,13 +3,14 @@
 //
 // These calls run once a layer and a step, at sizes where the kernels take a few
 // microseconds: in Python the same checks and allocations cost 11 to 20 us a call, here 2
-// to 6.  The library is not linked: fa.py hands over the addresses of its entry points, so
+// to 5.  The library is not linked: fa.py hands over the addresses of its entry points, so
 // that whatever build it has loaded is the one that runs.
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 
 #include <cmath>
 #include <cstdint>
@@ -108,8 +109,9 @@ Tensor aligned(const Tensor& t) {
   const Tensor c = t.contiguous();
   return at16(c) ? c : c.clone();
 }
+// (Past the dispatcher: 0.3 us less a tensor, 9.7 and 8.4 us for page extension's five.)
 Tensor empty(const Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
-  return at::empty(sizes, like.options().dtype(type));
+  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
 // t [..., H, D] as the library reads token-major rows: t itself where each token's heads
