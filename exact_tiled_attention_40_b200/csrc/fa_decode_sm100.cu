@@ -96,6 +96,11 @@ constexpr int dyn_unit(bool shared) { return shared ? 4 : kDynUnit; }
 constexpr int kMaxUnitsPerCta = 4;
 constexpr int kMaxStreamCtas = 204;                       // so a sequence has <= 1024 partials
 constexpr int kMaxMergeSlots = kMaxStreamCtas * (1 + kMaxUnitsPerCta);
+// SHARED, nothing attended together: a list of at most this many sequences, too short for
+// dynamic units, is summed up by every CTA itself instead of a kernel of its own (8 + 2
+// heads, us with that kernel / so: 7 sequences of 65 pages 13.4 / 11.3, 64 of 15 17.6 / 15.9,
+// but 256 of 3 19.6 / 20.4).
+constexpr int kScanHere = 128;
 constexpr int merge_warps(bool shared) { return shared ? 8 : 32; }
 constexpr int kHbSmemMax = 4096;   // sequences whose offsets the producer keeps in shared memory
 
@@ -124,6 +129,7 @@ struct DecodeParams {
   const float* pre_o;          // SHARED: segments' partial outputs [slot][256][128]
   const float* pre_lse;        // SHARED: their LSE [slot][256]
   const int32_t* prefix_table; // SHARED: ids of the shared pages
+  bool scan_here;              // SHARED: a short list, without a scan kernel (see kScanHere)
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -170,6 +176,16 @@ __device__ __forceinline__ OwnKeys own_keys(int len, int shared) {
     k.page0 = shared;
   }
   return k;
+}
+
+// SHARED, short list: pages of entry b, and the CTAs that share H of them.
+__device__ __forceinline__ int listed_pages(const DecodeParams& p, int b, bool flag) {
+  const int len = checked_len(p, b / p.groups);
+  if (len < 0 && flag) atomicOr(p.err, kErrBadIndex);
+  return len < 0 ? 0 : (len + kPage - 1) / kPage;
+}
+__device__ __forceinline__ int short_list_ctas(const DecodeParams& p, int H) {
+  return min(p.nctas, max(1, H / kOwnMinPages));
 }
 
 // Fold G partial sums held by 16 lanes (lane bits 0-3 = sub) into one full sum
@@ -493,22 +509,29 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // after the scan has finished; its own output is not read here, so this grid starts
   // on every SM that one has left and waits for it at the very end.
   // (Where the shared keys are streamed like the others, it does not stand there.)
+  // (With a short list this is the first kernel of the call.)
   if (!SHARED || !p.pw.together) pdl_wait();
   // The merge kernel may launch once every CTA is past this point, so its launch
   // implies that the scan has finished: it reads the offsets before its own wait.
   pdl_launch_dependents();
   // C: the CTAs with shares of the list
-  int shared = 0, listed = 0, C = gridDim.x;
-  if constexpr (SHARED) {
-    const PrefixSplit ps = prefix_split(p.pw, C);
-    shared = ps.pages;
-    C = ps.own_ctas;
-    if (!p.pw.together) listed = shared_pages(p.pw);   // pages to be read by prefix_table
-  }
-  const int H = SHARED ? __ldcg(p.hb + p.B) : p.hb[p.B];
-  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap, gridDim.x);
+  const bool scan_here = SHARED && p.scan_here;
+  int shared = 0, listed = 0, C = gridDim.x, H = 0;
+  StreamSplit sp = {1, 0, 1};
   Share own = {0, 0, 0};
-  if (c < C) own = share_of(c, H, C, sp);
+  if constexpr (SHARED) {
+    if (!p.pw.together) listed = shared_pages(p.pw);   // pages to be read by prefix_table
+    if (!scan_here) {
+      const PrefixSplit ps = prefix_split(p.pw, C);
+      shared = ps.pages;
+      C = ps.own_ctas;
+    }
+  }
+  if (!scan_here) {
+    H = SHARED ? __ldcg(p.hb + p.B) : p.hb[p.B];
+    sp = stream_split<SHARED>(H, C, p.dyn_units_cap, gridDim.x);
+    if (c < C) own = share_of(c, H, C, sp);
+  }
   __syncthreads();
 
   if (warp >= kConsumerWarps) {
@@ -520,7 +543,24 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const int* hbp = p.hb;
     if (p.hb_in_smem) {
       int* hb_sm = reinterpret_cast<int*>(dsm_raw + (sbase - smem_u32(dsm_raw)) + NS * 2 * SKV);
-      for (int i = lane; i <= p.B; i += 32) hb_sm[i] = __ldcg(p.hb + i);
+      if (scan_here) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+          const int v = b0 + lane < p.B ? listed_pages(p, b0 + lane, c == 0) : 0;
+          int x = v;                             // inclusive warp scan
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+          }
+          if (b0 + lane < p.B) hb_sm[b0 + lane] = H + x - v;
+          H += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) hb_sm[p.B] = H;
+        C = short_list_ctas(p, H);
+        if (c < C) own = share_of(c, H, C, sp);
+      } else {
+        for (int i = lane; i <= p.B; i += 32) hb_sm[i] = __ldcg(p.hb + i);
+      }
       __syncwarp();
       hbp = hb_sm;
     }
@@ -898,10 +938,41 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
   const int b = blockIdx.x;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int xs = __ldcg(p.hb + b), xe = __ldcg(p.hb + b + 1);
+  int xs, xe, H;                               // the entry's part of the list, its length
+  const bool scan_here = SHARED && p.scan_here;
+  if (scan_here) {
+    __shared__ int sums[3];
+    if (threadIdx.x < 3) sums[threadIdx.x] = 0;
+    __syncthreads();
+    int before = 0, mine = 0, total = 0;
+    for (int i = threadIdx.x; i < p.B; i += kWarps * 32) {
+      const int n = listed_pages(p, i, false);
+      total += n;
+      if (i < b) before += n;
+      if (i == b) mine = n;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) {
+      atomicAdd(&sums[0], before);
+      atomicAdd(&sums[1], mine);
+      atomicAdd(&sums[2], total);
+    }
+    __syncthreads();
+    xs = sums[0];
+    xe = xs + sums[1];
+    H = sums[2];
+  } else {
+    xs = __ldcg(p.hb + b);
+    xe = __ldcg(p.hb + b + 1);
+    H = __ldcg(p.hb + p.B);
+  }
   PrefixSplit ps = {};
   bool sees = false;                           // the sequence has the shared keys
-  if constexpr (SHARED) {
+  if (scan_here) {
+    ps.own_ctas = short_list_ctas(p, H);
+  } else if constexpr (SHARED) {
     ps = prefix_split(p.pw, p.pw.ctas);
     sees = ps.pages > 0 && checked_len(p, seq_of<SHARED>(p, b)) >= ps.pages * kPage;
   }
@@ -914,9 +985,9 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
     }
     return;
   }
-  const int H = __ldcg(p.hb + p.B);
   const int C = SHARED ? ps.own_ctas : p.nctas;
-  const StreamSplit sp = stream_split<SHARED>(H, C, p.dyn_units_cap, p.nctas);
+  StreamSplit sp = {1, 0, 1};
+  if (!scan_here) sp = stream_split<SHARED>(H, C, p.dyn_units_cap, p.nctas);
   if (warp == 0) {
     int base = 0;
     // no own keys: an empty range
@@ -1081,6 +1152,7 @@ int sm_count(int device) {
 // workspace of its segments.
 struct SharedPrefix {
   int B = 0, Hq = 0, Hkv = 0, groups = 1;      // of the call; head groups of a sequence
+  bool scan_here = false;
   const int32_t* table = nullptr;
   PrefixWork work;
   float* ws_o = nullptr;
@@ -1172,7 +1244,7 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    fa_decode_scan_kernel<SHARED><<<1, 1024, 0, stream>>>(prm);
+    if (!prm.scan_here) fa_decode_scan_kernel<SHARED><<<1, 1024, 0, stream>>>(prm);
     if constexpr (SHARED) {
       // right after the scan, overlapping it and the stream kernel
       if (prm.pw.together) {
@@ -1185,7 +1257,9 @@ int launch_kernels(const DecodeParams& prm, const DecodePlan& pl, const CUtensor
     cfg.gridDim = dim3(pl.nctas);
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = smem;
+    cfg.numAttrs = prm.scan_here ? 0 : 1;        // (then the call's first kernel)
     cudaLaunchKernelEx(&cfg, fa_decode_stream_kernel<G, SHARED>, tmK, tmV, prm);
+    cfg.numAttrs = 1;
     constexpr int mw = merge_warps(SHARED);
     cfg.gridDim = dim3(prm.B, SHARED ? (prm.Hq * prm.merge_split + mw - 1) / mw : 1);
     cfg.blockDim = dim3(mw * 32);
@@ -1234,6 +1308,7 @@ int run_decode(const void* q, const void* kcache, const void* vcache, const int3
   prm.pw = PrefixWork{};
   prm.pre_o = prm.pre_lse = nullptr;
   prm.prefix_table = pre ? pre->table : nullptr;
+  prm.scan_here = pre && pre->scan_here;
   if (pre) {
     prm.pw = pre->work;
     prm.pw.err = prm.err;
@@ -1353,9 +1428,12 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   pre.work.items = static_cast<int>(items);
   // Few copies of few shared pages are streamed with the own ones: the copies come from L2,
   // and the prefix kernel's start and end cost about 7 us.  32 + 8 heads, together / apart:
-  // 7 sequences of 32 pages 17.2 / 13.8 us, of 130 19.0 / 17.3, of 260 20.3 / 22.2;
-  // 64 of 16 19.5 / 18.6, of 32 20.2 / 26.7.
-  pre.work.together = entries * max_prefix_pages > 1024;
+  // 7 sequences of 32 pages 17.2 / 12.2 us, of 130 19.0 / 15.5, of 260 20.3 / 20.2;
+  // 64 of 16 19.5 / 17.7, of 32 20.2 / 24.7.
+  pre.work.together = entries * max_prefix_pages > 1536;
+  // (64 pages a CTA are the least of which a 16th makes a dynamic unit)
+  pre.scan_here = !pre.work.together && entries <= kScanHere &&
+                  entries * max_pages_per_seq < 64LL * pl.nctas;
   // Measured on an SM: a key tile against two row tiles 1.9 to 2.3 us, against one 1.8 us;
   // a page of 8 KV heads 0.92 us.  What matters is their ratio.  us of 256 sequences with
   // 32768 shared keys / 64 with 4096 at 2050 and 350 ns: 318 / 106, 700: 181 / 106, 1000:

@@ -109,8 +109,9 @@ def spread(seed, B, hi):
     (1, 1, 1, 1, 1), (1, 8, 2, 8, 40), (2, 8, 8, 9, 0), (5, 16, 2, 7, 33), (7, 8, 2, 65, 200),
     (33, 16, 16, 12, 50), (64, 32, 8, 16, 100), (65, 4, 1, 40, 20), (129, 4, 2, 3, 17),
     (257, 8, 8, 5, 20), (40, 64, 8, 33, 30), (3, 10, 5, 130, 9), (300, 8, 1, 17, 3),
-    (70, 9, 9, 16, 40), (5, 22, 11, 220, 30), (600, 8, 1, 2, 5), (9, 32, 16, 120, 90),
-    (2, 8, 8, 520, 70), (4200, 4, 1, 1, 20), (2, 8, 1, 600, 30000), (3, 64, 64, 50, 40)])
+    (70, 9, 9, 16, 40), (5, 22, 11, 220, 30), (600, 8, 1, 3, 5), (9, 32, 16, 120, 90),
+    (2, 8, 8, 800, 70), (4200, 4, 1, 1, 20), (2, 8, 1, 800, 30000), (3, 64, 64, 70, 40),
+    (128, 8, 2, 10, 90), (129, 8, 2, 10, 90), (257, 8, 8, 7, 20)])
 def test_matches_the_oracle(cuda_device, B, Hq, Hkv, P, hi):
     s = make(B + P, B, Hq, Hkv, P, spread(P, B, hi), cuda_device)
     o, lse = fa.decode_shared_prefix(*on_device(s, cuda_device))
@@ -120,7 +121,7 @@ def test_matches_the_oracle(cuda_device, B, Hq, Hkv, P, hi):
 # a few copies of the shared keys are streamed with the own ones, many are attended at
 # once; 16 KV heads go through the stream kernel in two groups
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-@pytest.mark.parametrize("P", [25, 90])
+@pytest.mark.parametrize("P", [25, 140])
 def test_shorter_sequences_and_padding_rows(cuda_device, Hq, Hkv, P):
     own = np.array([-16 * P, -1, 0, 1, 15, 16, 17, -384, -16, 1 - 16 * P, 250, -16 * P])
     s = make(3, 12, Hq, Hkv, P, own, cuda_device)
@@ -129,7 +130,7 @@ def test_shorter_sequences_and_padding_rows(cuda_device, Hq, Hkv, P):
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-@pytest.mark.parametrize("P", [4, 230])
+@pytest.mark.parametrize("P", [4, 320])
 def test_all_rows_empty(cuda_device, Hq, Hkv, P):
     s = make(4, 5, Hq, Hkv, P, [-16 * P] * 5, cuda_device)
     check(*fa.decode_shared_prefix(*on_device(s, cuda_device)), s)
@@ -137,14 +138,14 @@ def test_all_rows_empty(cuda_device, Hq, Hkv, P):
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
 def test_count_below_its_bound_and_none_shared(cuda_device, Hq, Hkv):
-    for P, bound in ((3, 50), (0, 50), (0, 0), (3, 130), (0, 130)):
+    for P, bound in ((3, 50), (0, 50), (0, 0), (3, 180), (0, 180)):
         s = make(5, 9, Hq, Hkv, P, spread(1, 9, 70), cuda_device, max_prefix=bound)
-        s["table"] = np.pad(s["table"], ((0, 0), (0, 130)))
+        s["table"] = np.pad(s["table"], ((0, 0), (0, 180)))
         check(*fa.decode_shared_prefix(*on_device(s, cuda_device)), s)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-@pytest.mark.parametrize("P", [10, 190])
+@pytest.mark.parametrize("P", [10, 270])
 def test_a_row_of_the_block_table_as_the_prefix(cuda_device, Hq, Hkv, P):
     s = make(6, 6, Hq, Hkv, P, spread(2, 6, 40), cuda_device)
     q, kc, vc, _, lens, _, pages = on_device(s, cuda_device)
@@ -153,7 +154,7 @@ def test_a_row_of_the_block_table_as_the_prefix(cuda_device, Hq, Hkv, P):
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
-@pytest.mark.parametrize("P", [10, 190])
+@pytest.mark.parametrize("P", [10, 270])
 def test_counts_and_ids_out_of_range(cuda_device, Hq, Hkv, P):
     s = make(7, 6, Hq, Hkv, P, spread(3, 6, 40), cuda_device)
     q, kc, vc, _, lens, prefix, pages = on_device(s, cuda_device)
@@ -173,7 +174,7 @@ def test_counts_and_ids_out_of_range(cuda_device, Hq, Hkv, P):
         check(o, lse, z)
 
 
-@pytest.mark.parametrize("P", [20, 270])
+@pytest.mark.parametrize("P", [20, 400])
 def test_lowest_and_infinite_scores(cuda_device, P):
     """Scores of -inf over the whole prefix: it takes no weight; large scores saturate."""
     s = make(8, 4, 8, 2, P, np.array([5, 0, 40, 1]), cuda_device, garbage=False)
@@ -195,7 +196,7 @@ def test_lowest_and_infinite_scores(cuda_device, P):
     assert fa.device_status() == 0
 
 
-@pytest.mark.parametrize("P", [50, 60])
+@pytest.mark.parametrize("P", [50, 80])
 def test_equal_to_plain_decode_without_lse(cuda_device, P):
     """The same numbers as fa_decode_paged within both calls' roundings."""
     s = make(9, 20, 32, 8, P, spread(4, 20, 300), cuda_device)
@@ -249,7 +250,7 @@ def test_long_prefix_over_every_sm(cuda_device):
 def test_graphs_streams_and_calls_at_once(cuda_device, Hq, Hkv):
     """Two captured graphs replayed at once on two streams, beside eager calls."""
     dev = cuda_device
-    cases = [make(11, 30, Hq, Hkv, 40, spread(5, 30, 90), dev),
+    cases = [make(11, 30, Hq, Hkv, 60, spread(5, 30, 90), dev),
              make(12, 11, Hq, Hkv, 90, spread(6, 11, 200), dev)]
     ins = [on_device(s, dev) for s in cases]
     for a in ins:
@@ -275,7 +276,7 @@ def test_graphs_streams_and_calls_at_once(cuda_device, Hq, Hkv):
     s = cases[0]
     short = dict(s, lens=s["lens"].copy(), own=s["own"].copy())
     short["own"] = np.minimum(short["own"], 16)
-    short["lens"] = 640 + short["own"]           # (40 shared pages)
+    short["lens"] = 960 + short["own"]           # (60 shared pages)
     ins[0][4].copy_(i32(short["lens"], dev))
     graphs[0].replay()
     check(*outs[0], short)

@@ -154,7 +154,7 @@ def test_extend_between_margins(cuda_device, B, new, rows):
     assert fa.device_status() == 0
 
 
-@pytest.mark.parametrize("Hq,Hkv,P", [(8, 2, 9), (8, 2, 200), (16, 16, 100), (6, 3, 250)])
+@pytest.mark.parametrize("Hq,Hkv,P", [(8, 2, 9), (8, 2, 230), (16, 16, 120), (6, 3, 250)])
 def test_shared_prefix_between_margins(cuda_device, Hq, Hkv, P):
     """Lengths that are not allowed among the others, margins around everything."""
     dev, B = cuda_device, 7
