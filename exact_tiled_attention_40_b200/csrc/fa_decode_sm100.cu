@@ -352,12 +352,12 @@ __global__ void __launch_bounds__(kDecThreads) fa_decode_split_kernel(const Deco
       const size_t base = (static_cast<size_t>(b) * p.nsplit + split) * p.Hq + hq0;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+        const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];      // 0: no key (a NaN is one)
         float4* dst = reinterpret_cast<float4*>(p.ws_o + (base + h) * kDecD + sub * 8);
         dst[0] = make_float4(acc[h][0] * inv, acc[h][1] * inv, acc[h][2] * inv, acc[h][3] * inv);
         dst[1] = make_float4(acc[h][4] * inv, acc[h][5] * inv, acc[h][6] * inv, acc[h][7] * inv);
         if (sub == 0)
-          p.ws_lse[base + h] = l[h] > 0.f ? (m[h] + __log2f(l[h])) * kLn2 : -INFINITY;
+          p.ws_lse[base + h] = l[h] == 0.f ? -INFINITY : (m[h] + __log2f(l[h])) * kLn2;
       }
     }
   }
@@ -808,14 +808,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         l_tot += __shfl_xor_sync(0xffffffffu, l_tot, 1);
         l_tot += __shfl_xor_sync(0xffffffffu, l_tot, 2);
         if (my_row) {
-          const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
+          const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // 0: no key (a NaN is one)
           const size_t rowi = (static_cast<size_t>(md.slot0) + md.b) * p.Hq + hq;
           float* dst = p.ws_o + rowi * kDecD + 2 * tq;
 #pragma unroll
           for (int nn = 0; nn < 16; ++nn)
             *reinterpret_cast<float2*>(dst + 8 * nn) = make_float2(o[nn][0] * inv, o[nn][1] * inv);
           if (tq == 0)
-            p.ws_lse[rowi] = l_tot > 0.f ? (m_run + __log2f(l_tot)) * kLn2 : -INFINITY;
+            p.ws_lse[rowi] = l_tot == 0.f ? -INFINITY : (m_run + __log2f(l_tot)) * kLn2;
         }
       }
     }
@@ -840,7 +840,9 @@ constexpr int kMergeBatch = 8;
 // n partial results of one (sequence, query head) joined by their LSE: lse_at(k) and
 // row_at(k) (the lane's four columns) give the k-th.  32 partials at a time (one
 // sequence rarely has more): one LSE per lane and the first kMergeBatch rows load
-// together; a later chunk with a larger maximum rescales what is accumulated so far.
+// together; a later chunk with a larger maximum rescales what is accumulated so far.  A
+// partial whose scores had a NaN has a NaN LSE, which the maximum passes over and the sum
+// of the weights takes up: only partials with an LSE of -inf, those of no key, are nothing.
 struct Joined {
   float4 acc;       // the lane's columns, weighted by exp(LSE - mx)
   float wsum, mx;   // sum of the weights (all lanes), their reference
@@ -860,7 +862,8 @@ __device__ __forceinline__ Joined join_partials(int n, int lane, LseAt lse_at, R
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     m = fmaxf(m, mx);
-    if (m == -INFINITY) continue;              // every LSE so far is -inf (warp-uniform)
+    // every LSE so far is -inf (warp-uniform)
+    if (m == -INFINITY && !__any_sync(0xffffffffu, ls != -INFINITY)) continue;
     const float sc = ex2((mx - m) * kLog2e);   // 0 on the first finite chunk
     acc.x *= sc;
     acc.y *= sc;
@@ -893,10 +896,10 @@ __device__ __forceinline__ Joined join_partials(int n, int lane, LseAt lse_at, R
   return {acc, wsum, mx};
 }
 __device__ __forceinline__ void store_joined(const Joined& r, int lane, uint16_t* o, float* lse) {
-  const float inv = r.wsum > 0.f ? 1.f / r.wsum : 0.f;
+  const float inv = r.wsum == 0.f ? 0.f : 1.f / r.wsum;
   *reinterpret_cast<uint2*>(o + lane * 4) = make_uint2(
       pack_bf16x2(r.acc.x * inv, r.acc.y * inv), pack_bf16x2(r.acc.z * inv, r.acc.w * inv));
-  if (lse && lane == 0) *lse = r.wsum > 0.f ? r.mx + __log2f(r.wsum) * kLn2 : -INFINITY;
+  if (lse && lane == 0) *lse = r.wsum == 0.f ? -INFINITY : r.mx + __log2f(r.wsum) * kLn2;
 }
 
 // The segments of the shared prefix that hold row (b, h): n of them, the k-th at row
@@ -1059,6 +1062,7 @@ __global__ void __launch_bounds__(merge_warps(SHARED) * 32) fa_decode_stream_mer
         float mx = r.mx;
         for (int i = 1; i < split; ++i) mx = fmaxf(mx, parts[warp + i][lane].mx);
         Joined all = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f, mx};
+        // (a NaN in a part without a finite LSE stays one under its weight of zero)
         for (int i = 0; i < split; ++i) {
           const Joined q = parts[warp + i][lane];
           const float w = q.mx == -INFINITY ? 0.f : ex2((q.mx - mx) * kLog2e);
@@ -1090,8 +1094,13 @@ __global__ void __launch_bounds__(kDecD) fa_decode_combine_kernel(const DecodePa
   if (ns > 0) {
     const size_t base = static_cast<size_t>(b) * p.nsplit * p.Hq + h;
     float mx = -INFINITY;
-    for (int s = 0; s < ns; ++s) mx = fmaxf(mx, p.ws_lse[base + static_cast<size_t>(s) * p.Hq]);
-    if (mx > -INFINITY) {
+    bool any = false;                          // a partial with keys (a NaN's LSE is NaN)
+    for (int s = 0; s < ns; ++s) {
+      const float ls = p.ws_lse[base + static_cast<size_t>(s) * p.Hq];
+      any |= ls != -INFINITY;
+      mx = fmaxf(mx, ls);
+    }
+    if (any) {
       float wsum = 0.f, acc = 0.f;
       for (int s = 0; s < ns; ++s) {
         const size_t idx = base + static_cast<size_t>(s) * p.Hq;

@@ -274,7 +274,8 @@ int fa_merge_partials(float* o_acc, float* lse_acc, const void* o_part, const fl
  * Supported: D == 128, page_size == 16, Hq / Hkv in {1, 2, 4, 8}.
  * num_pages bounds every block-table entry (0 <= id < num_pages); entries out
  * of range are skipped and flagged in the device error word.
- * A sequence of length 0 gets O = 0 and LSE = -inf.
+ * A sequence of length 0 gets O = 0 and LSE = -inf.  A row with a NaN among its
+ * scores gets NaN in all of O and in LSE.
  * Work is split over key chunks; partial results are merged by their LSE.
  * For Hkv <= 8 one persistent CTA per SM takes an equal share of all
  * sequences' cache (so ragged lengths stay balanced); otherwise the grid is
