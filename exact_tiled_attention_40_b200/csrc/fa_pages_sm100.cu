@@ -294,7 +294,8 @@ int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device) {
   if (e == cudaSuccess && !prm.rows) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(std::min((a.max_tokens + kRowThreads - 1) / kRowThreads, 2 * nsm));
+    // (max_tokens > 0 here, and close to 2^31 at most: nothing is added to it)
+    cfg.gridDim = dim3(std::min(1 + (a.max_tokens - 1) / kRowThreads, 2 * nsm));
     cfg.blockDim = dim3(kRowThreads);
     cfg.dynamicSmemBytes = (a.B + 1) * static_cast<int>(sizeof(int));
     e = cudaLaunchKernelEx(&cfg, fa_extend_rows_kernel, prm);
