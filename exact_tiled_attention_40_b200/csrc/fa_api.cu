@@ -31,6 +31,9 @@ int set_error(int code, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
   va_end(ap);
+  // The runtime keeps the error of a failed call for whoever asks next, and the launches
+  // ask after themselves: it is reported here and must not be the next call's as well.
+  if (code == FA_ERR_CUDA || code == FA_ERR_NO_DEVICE) cudaGetLastError();
   return code;
 }
 
@@ -140,10 +143,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int current_sm100(int* dev) {
   int d = -1;
   cudaError_t e = cudaGetDevice(&d);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
+  if (e != cudaSuccess)
     return set_error(FA_ERR_NO_DEVICE, "no CUDA device: %s", cudaGetErrorString(e));
-  }
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d);

@@ -1391,7 +1391,10 @@ int launch_decode(const void* q, const void* kcache, const void* vcache, const i
   rc = run_decode(q, kcache, vcache, block_table, seq_lens, o, lse, B, Hq, Hkv, max_pages_per_seq,
                   num_pages, scale, pl, ws, stream, device);
   cudaError_t ef = cudaFreeAsync(ws, stream);
-  if (rc != FA_OK) return rc;
+  if (rc != FA_OK) {
+    cudaGetLastError();                // of the release: the first error is the one reported
+    return rc;
+  }
   if (ef != cudaSuccess)
     return set_error(FA_ERR_CUDA, "workspace release: %s", cudaGetErrorString(ef));
   return FA_OK;
@@ -1468,7 +1471,10 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
                   max_pages_per_seq, num_pages, scale, pl, static_cast<char*>(ws) + pre_bytes,
                   stream, device, &pre);
   cudaError_t ef = cudaFreeAsync(ws, stream);
-  if (rc != FA_OK) return rc;
+  if (rc != FA_OK) {
+    cudaGetLastError();                // of the release: the first error is the one reported
+    return rc;
+  }
   if (ef != cudaSuccess)
     return set_error(FA_ERR_CUDA, "workspace release: %s", cudaGetErrorString(ef));
   return FA_OK;

@@ -300,7 +300,6 @@ int launch_extend_pages(const ExtendArgs& a, cudaStream_t stream, int device) {
     cfg.dynamicSmemBytes = (a.B + 1) * static_cast<int>(sizeof(int));
     e = cudaLaunchKernelEx(&cfg, fa_extend_rows_kernel, prm);
   }
-  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     return set_error(FA_ERR_CUDA, "page extension launch: %s", cudaGetErrorString(e));
   return FA_OK;
