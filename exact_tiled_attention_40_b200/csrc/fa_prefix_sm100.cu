@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]), p.err);
         tmem_wait_ld(p.err);
         const int kbase = (s.j0 + j) * kBN;
-        if (kbase + kBN > n_keys) {              // the prefix ends inside this tile
+        if (n_keys - kbase < kBN) {              // the prefix ends inside this tile
           const int lim = n_keys - 1 - kbase;
 #pragma unroll
           for (int e = 0; e < 128; ++e)

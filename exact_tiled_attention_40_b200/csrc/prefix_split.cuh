@@ -36,6 +36,13 @@ __device__ __forceinline__ int shared_pages(const PrefixWork& w) {
   return n;
 }
 
+// Key tiles of so many shared pages (whose tokens may be close to 2^31).
+__host__ __device__ constexpr int prefix_tiles(int pages) {
+  constexpr int kTilePages = kPrefixTile / 16;
+  return pages / kTilePages + (pages % kTilePages != 0);
+}
+static_assert(prefix_tiles(0x7fffffff / 16) == 1 << 24, "the longest prefix");
+
 // A unit is a key tile of a KV head for a team of CTAs, each of which takes a pair of row
 // tiles: they read the same keys at about the same time, so that HBM is read once and not
 // once a pair (256 sequences of 32 + 8 heads, 4 pairs a KV head, 32768 shared keys: 178.0
@@ -56,7 +63,7 @@ struct PrefixSplit {
 __device__ __forceinline__ PrefixSplit prefix_split(const PrefixWork& w, int C) {
   PrefixSplit s;
   s.pages = w.together ? shared_pages(w) : 0;
-  s.nt = (s.pages * 16 + kPrefixTile - 1) / kPrefixTile;
+  s.nt = prefix_tiles(s.pages);
   s.units = w.items * s.nt;
   const long long prefix = static_cast<long long>(s.units) * w.team * w.tile_ns;
   const int own_pages = __ldcg(w.own_total);
