@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
     fa_norm_rope_bwd_kernel(const BwdParams bp) {
   constexpr int LANES = D / 8, GROUPS = kBwdThreads / LANES;
   extern __shared__ uint4 pieces[];            // [stage][piece][thread]
-  __shared__ float sums[GROUPS][D];
+  __shared__ __align__(16) float sums[GROUPS][D];   // (written 16 bytes at a time)
+  static_assert(__alignof__(sums) >= 16 && D % 4 == 0, "alignment of the float4 stores");
   const RowParams& p = bp.r;
   const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const Lane<INTER> own(l, p.rot);
