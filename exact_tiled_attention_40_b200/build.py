@@ -4,7 +4,8 @@ Usage: ``python -m exact_tiled_attention_40_b200.build`` (or ``build()`` from
 Python).  Every .cu file under csrc/ is compiled with nvcc for sm_100a only and
 linked with the static CUDA runtime; the driver API is reached at run time
 through cudaGetDriverEntryPoint, so loading the library needs no GPU.  The
-compiled part of the Python binding, ``_step.so``, is built with g++ beside it.
+compiled part of the Python binding, ``_step.so``, is built with g++ beside it,
+where g++ and the headers of torch and Python are: the library needs neither.
 
 ``build(debug=True)`` (``--debug``) builds the same library with FA_DEBUG=1 into
 _build/debug/libfa_sm100.so: every tensor-memory load, store and wait first
@@ -15,6 +16,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -67,16 +69,36 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
     return obj
 
 
-def _build_binding() -> str:
-    """The Python module of csrc/py_step.cpp (it calls the library by address)."""
+def _binding_lacks(torch_dir: str | None, python_include: str) -> str | None:
+    """What building the binding would need and does not find here."""
+    if shutil.which("g++") is None:
+        return "g++"
+    if torch_dir is None:
+        return "torch"
+    for header in (os.path.join(torch_dir, "include", "torch", "csrc", "utils", "pybind.h"),
+                   os.path.join(python_include, "Python.h")):
+        if not os.path.exists(header):
+            return header
+    return None
+
+
+def _build_binding() -> str | None:
+    """The Python module of csrc/py_step.cpp (it calls the library by address); None, with
+    a note, where its tools are missing."""
     src = os.path.join(CSRC, "py_step.cpp")
     if _stale(BINDING, [src, os.path.join(ROOT, "include", "fa.h")]):
-        import torch
-        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        spec = importlib.util.find_spec("torch")
+        torch_dir = os.path.dirname(spec.origin) if spec else None
+        python_include = sysconfig.get_paths()["include"]
+        lacks = _binding_lacks(torch_dir, python_include)
+        if lacks:
+            print(f"the Python binding of the step operators is not built: no {lacks}",
+                  file=sys.stderr)
+            return None
+        lib, inc = os.path.join(torch_dir, "lib"), os.path.join(torch_dir, "include")
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-        paths = [inc, os.path.join(inc, "torch", "csrc", "api", "include"),
-                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        paths = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), python_include,
+                 os.path.join(cuda, "include")]
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                "-I", os.path.join(ROOT, "include"), *[f for p in paths for f in ("-isystem", p)],
                src, "-o", BINDING, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
@@ -94,12 +116,12 @@ def build(verbose_ptxas: bool = False, debug: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, debug), sources))
-    binding.result()
     if _stale(lib, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", lib, *objs, "-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    binding.result()                   # (raises what it failed with, behind the library)
     return lib
 
 
