@@ -18,6 +18,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -69,6 +70,21 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
     return obj
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
+
+
+def binding_abi() -> str:
+    """What a build of the binding belongs to: the versions of torch (read from its
+    version.py; importing it takes seconds) and of Python."""
+    version = "none"
+    if _torch_dir():
+        with open(os.path.join(_torch_dir(), "version.py")) as f:
+            version = re.search(r"__version__ = ['\"]([^'\"]+)", f.read()).group(1)
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
 def _binding_lacks(torch_dir: str | None, python_include: str) -> str | None:
     """What building the binding would need and does not find here."""
     if shutil.which("g++") is None:
@@ -86,10 +102,10 @@ def _build_binding() -> str | None:
     """The Python module of csrc/py_step.cpp (it calls the library by address); None, with
     a note, where its tools are missing."""
     src = os.path.join(CSRC, "py_step.cpp")
-    if _stale(BINDING, [src, os.path.join(ROOT, "include", "fa.h")]):
-        spec = importlib.util.find_spec("torch")
-        torch_dir = os.path.dirname(spec.origin) if spec else None
-        python_include = sysconfig.get_paths()["include"]
+    abi, stamp = binding_abi(), os.path.join(BUILD, "_step.abi")
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if built_for != abi or _stale(BINDING, [src, os.path.join(ROOT, "include", "fa.h")]):
+        torch_dir, python_include = _torch_dir(), sysconfig.get_paths()["include"]
         lacks = _binding_lacks(torch_dir, python_include)
         if lacks:
             print(f"the Python binding of the step operators is not built: no {lacks}",
@@ -100,12 +116,15 @@ def _build_binding() -> str | None:
         paths = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), python_include,
                  os.path.join(cuda, "include")]
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f'-DFA_BINDING_ABI="{abi}"',
                "-I", os.path.join(ROOT, "include"), *[f for p in paths for f in ("-isystem", p)],
                src, "-o", BINDING, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
                "-ltorch_cuda", "-ltorch_python"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+        with open(stamp, "w") as f:
+            f.write(abi)
     return BINDING
 
 

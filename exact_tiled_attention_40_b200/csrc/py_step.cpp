@@ -403,6 +403,7 @@ void bind(const py::dict& entry, const py::object& error) {
 }  // namespace
 
 PYBIND11_MODULE(_step, m) {
+  m.attr("abi") = FA_BINDING_ABI;      // the torch and the Python that it was compiled for
   m.def("bind", &bind);
   m.def("head_rows", &head_rows);
   m.def("qk_norm_rope", &qk_norm_rope);

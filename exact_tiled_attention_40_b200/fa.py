@@ -15,6 +15,8 @@ import re
 
 import torch
 
+from .build import binding_abi
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 # FA_LIBRARY may name another build of the same ABI (e.g. the FA_DEBUG build).
 LIB_PATH = os.environ.get("FA_LIBRARY") or os.path.join(HERE, "libfa_sm100.so")
@@ -129,6 +131,10 @@ def _native():
         except ImportError as e:
             raise FAError(-1, "load", f"the compiled binding is missing or does not load ({e}); run "
                           "`python -m exact_tiled_attention_40_b200.build`")
+        built_for = getattr(module, "abi", "another version of this package")
+        if built_for != binding_abi():
+            raise FAError(-1, "load", f"the compiled binding was built for {built_for}, this is "
+                          f"{binding_abi()}; run `python -m exact_tiled_attention_40_b200.build`")
         l = lib()
         module.bind({name: ctypes.cast(getattr(l, name), ctypes.c_void_p).value
                      for name in _SIGS}, FAError)

@@ -84,3 +84,33 @@ def test_a_library_that_does_not_compile_fails(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         b.build()
     assert not (tree / "lib.so").exists()
+
+
+def test_the_binding_is_rebuilt_for_another_torch(tree, monkeypatch):
+    run = Run()
+    use(monkeypatch, run)
+    b.build()
+    run.outputs.clear()
+    monkeypatch.setattr(b, "binding_abi", lambda: "torch 0.0.1, another Python")
+    b.build()
+    assert run.outputs == ["_step.so"]
+    run.outputs.clear()
+    b.build()
+    assert run.outputs == []
+
+
+def test_the_build_is_for_the_running_torch_and_python():
+    import sys
+    import torch
+    assert torch.__version__ in b.binding_abi() and sys.implementation.cache_tag in b.binding_abi()
+
+
+def test_a_binding_of_another_torch_is_refused(monkeypatch):
+    from exact_tiled_attention_40_b200 import fa
+    monkeypatch.setattr(fa, "_step", None)
+    fa._native()                                 # (this tree's own loads)
+    monkeypatch.setattr(fa, "_step", None)
+    monkeypatch.setattr(fa, "binding_abi", lambda: "torch 0.0.1, another Python")
+    with pytest.raises(fa.FAError, match="another Python"):
+        fa._native()
+    assert fa._step is None
