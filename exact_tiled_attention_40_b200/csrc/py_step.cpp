@@ -176,11 +176,11 @@ struct NormRope {
     max_pos = tab.size(0);
     rot = tab.size(1);
     dtype(where, "positions", pos, at::kInt);
-    axes = pos.dim() == 1 ? 1 : pos.size(0);
     if (pos.dim() == 1)
       shape(where, "positions", pos, {tokens});
     else
       shape(where, "positions", pos, {-1, tokens});
+    axes = pos.dim() == 1 ? 1 : pos.size(0);
     if (axes != 1) {
       if (!axis)
         refuse(FA_ERR_INVALID_ARG, where, "pair_axis is needed with more than one axis");
