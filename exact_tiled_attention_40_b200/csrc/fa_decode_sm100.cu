@@ -1439,7 +1439,8 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   pre.work.pairs = static_cast<int>(pairs);
   pre.work.items = static_cast<int>(items);
   // Few copies of few shared pages are streamed with the own ones: the copies come from L2,
-  // and the prefix kernel's start and end cost about 7 us.  32 + 8 heads, together / apart:
+  // and the prefix kernel's start and end cost about 7 us.  The launches are chosen here, by
+  // the bound on the pages; the count itself is on the device.  32 + 8 heads, together / apart:
   // 7 sequences of 32 pages 17.2 / 12.2 us, of 130 19.0 / 15.5, of 260 20.3 / 20.2;
   // 64 of 16 19.5 / 17.7, of 32 20.2 / 24.7.
   pre.work.together = entries * max_prefix_pages > 1536;
@@ -1447,7 +1448,8 @@ int launch_decode_shared(const void* q, const void* kcache, const void* vcache,
   pre.scan_here = !pre.work.together && entries <= kScanHere &&
                   entries * max_pages_per_seq < 64LL * pl.nctas;
   // Measured on an SM: a key tile against two row tiles 1.9 to 2.3 us, against one 1.8 us;
-  // a page of 8 KV heads 0.92 us.  What matters is their ratio.  us of 256 sequences with
+  // a page of 8 KV heads 0.92 us (of 4 or fewer 0.68: one number for all counts those a
+  // quarter too dear).  What matters is their ratio.  us of 256 sequences with
   // 32768 shared keys / 64 with 4096 at 2050 and 350 ns: 318 / 106, 700: 181 / 106, 1000:
   // 170 / 107, 1400: 178 / 126, 2000: 190 / 150, 3000: 219 / 199; in a long run at the power
   // limit, where tiles take longer, 195 / 112 at 750 and 194 / 112 at 850.

@@ -17,8 +17,9 @@
 // is computed in fp32, in packed pairs, and rounded once.
 //
 // 8192 tokens of 32 + 8 heads of 128 in bf16 (events around graph replays, inputs of three
-// times L2): forward 32.5 us, 5.3 TB/s; with K and V to the pool 37.4 us, 5.5 TB/s;
-// backward 45.4 us, 5.6 TB/s (copy: 6.55 TB/s); 64 tokens to the pool 3.0 us.
+// times L2; each input and output byte counted once): forward 32.7 us, 5.3 TB/s; with K and V
+// to the pool 37.5 us, 5.5 TB/s; backward 45.5 us, 5.6 TB/s (copy: 6.55 TB/s); 64 tokens to
+// the pool 3.0 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -9,8 +9,8 @@
 // memory; the cluster then meets, so that the lengths and the page count may be written in
 // place, and its threads share the new pages, each finding its sequence by binary search.
 // Few token rows are dealt with by the same (one) CTA; many by a second grid over all SMs,
-// which reads what the first has written.  Bound by latency: 4.2 us for 64 sequences of
-// one token, 8.1 us for 301 with 262 k rows (one cluster for all: 24.1 us).
+// which reads what the first has written.  Bound by latency: 4.0-4.2 us for 64 sequences of
+// one token, 7.5-8.1 us for 301 with 262 k rows (one cluster for all: 24.1 us).
 #include <algorithm>
 
 #include "fa_internal.h"

@@ -50,8 +50,8 @@ static_assert(prefix_tiles(0x7fffffff / 16) == 1 << 24, "the longest prefix");
 //
 // The prefix kernel and the stream kernel are both bound by what an SM does (tiles, pages),
 // so the SMs are divided between them in proportion to their work: the teams' CTAs take
-// prefix tiles, and the stream kernel's blocks, as many as there are SMs left, which start at once on the
-// others, share the sequences' own pages.
+// prefix tiles, and the stream kernel's blocks, as many as there are SMs left, which start at
+// once on the others, share the sequences' own pages.
 struct PrefixSplit {
   int pages;       // shared pages that are attended at once
   int nt;          // key tiles of the prefix

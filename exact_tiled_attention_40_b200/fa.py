@@ -457,7 +457,9 @@ def decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
     """decode_paged for a batch whose sequences share their first pages: the first
     prefix_pages[0] (int32, on the device) entries of prefix_table [max_prefix_pages]
     (a row of block_table will do).  Sequences shorter than the shared pages take no
-    part and are read through their own block_table row."""
+    part and are read through their own block_table row.  How the work is launched goes
+    by the widths of the tables: a prefix_table no wider than the sharing can get is faster
+    for few sequences (see include/fa.h)."""
     return _native().decode_shared_prefix(q, kcache, vcache, block_table, seq_lens, prefix_table,
                                           prefix_pages, scale, return_lse)
 
@@ -525,7 +527,9 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table, posit
                           pair_axis=None, eps=1e-6, interleaved=False, heads_first=True):
     """(dq, dk, dq_weight, dk_weight) of qk_norm_rope for the gradients dq_out, dk_out of its
     outputs: dq [B, N, Hq, D] and dk [B, N, Hkv, D] in q's dtype, the weights' in fp32
-    (None where the weight is None)."""
+    (None where the weight is None).  fa_qk_norm_rope_bwd, the raw call, writes dq and dk
+    into views of one gradient of the projection instead.  In fp16 the gradients dq_out and
+    dk_out are the caller's: attention_backward is bf16 only."""
     return _native().qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, table,
                                            positions, pair_axis, eps, interleaved, heads_first)
 

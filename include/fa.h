@@ -349,6 +349,15 @@ int fa_decode_paged_noalloc(const void* q, const void* kcache, const void* vcach
  * A prefix_pages[0] outside [0, max_prefix_pages] raises FA_ERR_DEVICE_INDEX and
  * counts as 0; so does an id of the shared pages outside [0, num_pages), whose 16
  * keys then count as zero vectors.  The workspace is taken as by fa_decode_paged.
+ * The softmax weights are rounded to bf16 for their product with V, as in
+ * fa_decode_paged and fa_fwd (each by at most 2^-8 of itself); scores, maxima, sums
+ * and partial results are fp32.
+ * max_prefix_pages and max_pages_per_seq also choose the launches, since the count is on
+ * the device: up to 1536 pages of B * max_prefix_pages (times the groups of KV heads,
+ * where there are more than 8) are streamed with the own keys, more are attended
+ * together.  The results agree within rounding, the times of few sequences differ (7 that
+ * share 32 pages, 32 + 8 heads: 12 us; 15 in a block_table 2048 pages wide; 19 with a
+ * prefix_table of 512 or more), so give bounds as tight as they are known.
  */
 int fa_decode_shared_prefix(const void* q, const void* kcache, const void* vcache,
                             const int32_t* block_table, const int32_t* seq_lens,
@@ -452,7 +461,11 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
                         int n_axes, int interleaved, int heads_first, float eps,
                         fa_stream_t stream);
 
-/* Same as fa_qk_norm_rope_bwd with fp16 tensors and weights (fp32 dq_weight, dk_weight). */
+/*
+ * Same as fa_qk_norm_rope_bwd with fp16 tensors and weights (fp32 dq_weight, dk_weight).
+ * fa_bwd is bf16 only: dq_out and dk_out come from the caller's own fp16 attention
+ * backward (fa_fwd_fp16 gives its O and LSE).
+ */
 int fa_qk_norm_rope_bwd_fp16(const void* q, const void* k, const void* dq_out, const void* dk_out,
                              const void* q_weight, const void* k_weight, const float* table,
                              const int32_t* positions, const uint8_t* pair_axis, void* dq,
