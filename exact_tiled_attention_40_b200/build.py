@@ -72,17 +72,18 @@ def _compile(src: str, verbose_ptxas: bool, debug: bool = False) -> str:
 
 def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec else None
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
 def binding_abi() -> str:
     """What a build of the binding belongs to: the versions of torch (read from its
     version.py; importing it takes seconds) and of Python."""
-    version = "none"
-    if _torch_dir():
-        with open(os.path.join(_torch_dir(), "version.py")) as f:
-            version = re.search(r"__version__ = ['\"]([^'\"]+)", f.read()).group(1)
-    return f"torch {version}, {sys.implementation.cache_tag}"
+    path = os.path.join(_torch_dir() or "", "version.py")
+    version = None
+    if _torch_dir() and os.path.exists(path):
+        with open(path) as f:
+            version = re.search(r"__version__ = ['\"]([^'\"]+)", f.read())
+    return f"torch {version.group(1) if version else 'unknown'}, {sys.implementation.cache_tag}"
 
 
 def _binding_lacks(torch_dir: str | None, python_include: str) -> str | None:

@@ -114,3 +114,12 @@ def test_a_binding_of_another_torch_is_refused(monkeypatch):
     with pytest.raises(fa.FAError, match="another Python"):
         fa._native()
     assert fa._step is None
+
+
+def test_a_torch_that_does_not_say_its_version(tmp_path, monkeypatch):
+    monkeypatch.setattr(b, "_torch_dir", lambda: str(tmp_path))
+    assert "unknown" in b.binding_abi()
+    (tmp_path / "version.py").write_text("git_version = 'x'\n")
+    assert "unknown" in b.binding_abi()
+    monkeypatch.setattr(b, "_torch_dir", lambda: None)
+    assert "unknown" in b.binding_abi()
